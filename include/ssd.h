@@ -484,6 +484,183 @@ SSD_API const char* ssd_bwd_path(const ssd_bwd_args* args);
  * when a launch fails (outputs then undefined). */
 SSD_API ssd_status ssd_bwd(const ssd_bwd_args* args, void* stream);
 
+/* The gated delta rule: the linear recurrence next to the SSD in which a token
+ * replaces what the state answers to its key instead of adding to it.  Per
+ * batch row b and head h, with group g = h / (nheads / ngroups) sharing q and
+ * k as the SSD's heads share C and B:
+ *
+ *   u_t = beta_t (v_t - exp(g_t) S_{t-1} k_t)
+ *   S_t = exp(g_t) S_{t-1} + u_t k_t^T          state, headdim x dstate
+ *   y_t = scale S_t q_t                          output, headdim
+ *
+ * with S_{-1} = initial_states[b,h] (or 0).  v, the state and y have the
+ * layouts of the SSD's x, state and y.  With seq_idx every maximal run of one
+ * id in a row is a sequence of its own; the initial state enters the row's
+ * first one only.  The pages describe no such operator; it has no counterpart
+ * there.
+ *
+ * The result is computed in chunks of 32 tokens, whose triangular systems are
+ * inverted once and applied on the tensor cores; the operands carry 22 bits
+ * (11 for what only y's rounding to bf16 sees), the sums 32.  It equals the
+ * recurrence up to rounding.  Every input must be finite, but for g, where -inf is
+ * a decay of zero: a value that is not finite can make the outputs of its
+ * head from up to 31 tokens before it undefined.  Sizes: any dstate up to
+ * 256 and any headdim up to 65536, batch * seqlen below 2^31.  Tensors on
+ * 16-byte boundaries whose rows are multiples of 16 bytes are read with wide
+ * loads, others element by element. */
+typedef struct {
+  int64_t batch, seqlen, nheads, headdim, dstate, ngroups;
+  ssd_dtype dtype;             /* of q, k, v and y                               */
+  uint32_t flags;              /* SSD_FLAG_CHECK_SEQ or 0                        */
+  const void* q;               /* (b,L,G,N) dtype, queries                       */
+  const void* k;               /* (b,L,G,N) dtype, keys                          */
+  const void* v;               /* (b,L,H,P) dtype, values                        */
+  const float* g;              /* (b,L,H) fp32, log decay (expected <= 0)        */
+  const float* beta;           /* (b,L,H) fp32, step size                        */
+  const float* initial_states; /* (b,H,P,N) fp32, or NULL = 0                    */
+  const int32_t* seq_idx;      /* (b,L) int32 packed-sequence ids, or NULL.
+                                  Precondition: ids in [0, num_seqs), each one
+                                  run in one row (else outputs are undefined, but
+                                  for memory: nothing is written out of bounds)  */
+  int64_t num_seqs;            /* number of sequence ids; required iff seq_idx   */
+  void* y;                     /* (b,L,H,P) dtype, output                        */
+  float* final_states;         /* output or NULL: (b,H,P,N) fp32; with seq_idx
+                                  (num_seqs,H,P,N), zeros for absent ids         */
+  void* workspace;             /* ssd_delta_fwd_workspace_size bytes, 256-byte
+                                  aligned (NULL when that is 0); contents on
+                                  entry do not matter                            */
+  size_t workspace_bytes;
+  float scale;                 /* of y; dstate^-1/2 is usual                     */
+} ssd_delta_args;
+
+/* Workspace bytes ssd_delta_fwd needs (sizes, dtype and the presence of
+ * seq_idx only; 0 without seq_idx, or if the sizes are invalid). */
+SSD_API size_t ssd_delta_fwd_workspace_size(const ssd_delta_args* args);
+
+/* Enqueue the forward on `stream`: one kernel, and one before it with
+ * seq_idx.  SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_WORKSPACE as
+ * for ssd_fwd, with nothing enqueued; SSD_ERR_CUDA when a launch fails.
+ * Outputs must not overlap the inputs. */
+SSD_API ssd_status ssd_delta_fwd(const ssd_delta_args* args, void* stream);
+
+/* One token of the gated delta rule per batch row (decode) on a state held by
+ * the caller: the recurrence above once, state read and written in place.
+ * dstate a multiple of 4, at most 256 (else SSD_ERR_UNSUPPORTED); state and,
+ * per 4 elements, q and k aligned as for ssd_step.  Asynchronous on `stream`;
+ * nothing is enqueued when the arguments are rejected. */
+typedef struct {
+  int64_t batch, nheads, headdim, dstate, ngroups;
+  ssd_dtype dtype;   /* of q, k, v and y                     */
+  float scale;
+  const void* q;     /* (b,G,N) dtype                        */
+  const void* k;     /* (b,G,N) dtype                        */
+  const void* v;     /* (b,H,P) dtype                        */
+  const float* g;    /* (b,H) fp32                           */
+  const float* beta; /* (b,H) fp32                           */
+  float* state;      /* (b,H,P,N) fp32, in place             */
+  void* y;           /* (b,H,P) dtype, output                */
+} ssd_delta_step_args;
+
+SSD_API ssd_status ssd_delta_step(const ssd_delta_step_args* args, void* stream);
+
+/* The backward of ssd_delta_fwd: the gradients of a loss with respect to every
+ * input, given dy = dLoss/dy and optionally dfinal_states.  With G_t the
+ * gradient of S_t, swept from the last token, d_t = G_t k_t the gradient of
+ * u_t and e_t = v_t - exp(g_t) S_{t-1} k_t (u_t = beta_t e_t):
+ *
+ *   G_t     = scale dy_t q_t^T + exp(g_{t+1}) (G_{t+1} - beta_{t+1} d_{t+1} k_{t+1}^T)
+ *   dq_t    = sum over the group's heads of scale S_t^T dy_t
+ *   dk_t    = sum over the group's heads of G_t^T u_t - beta_t exp(g_t) S_{t-1}^T d_t
+ *   dv_t    = beta_t d_t
+ *   dbeta_t = <d_t, e_t>
+ *   dg_t    = exp(g_t) <G_t - beta_t d_t k_t^T, S_{t-1}>
+ *   dinitial_states = exp(g_0) (G_0 - beta_0 d_0 k_0^T)
+ *
+ * The states are recomputed from the inputs; what the forward returned is not
+ * read.  A gradient has its input's type, rounded once: dq, dk and dv dtype,
+ * the others fp32.  Every sum is taken in a fixed order, so results are
+ * deterministic.  Unlike ssd_bwd, gradients of per-sequence final states are
+ * taken. */
+typedef struct {
+  ssd_delta_args fwd;          /* sizes and inputs as for ssd_delta_fwd; its y,
+                                  final_states and workspace are ignored         */
+  const void* dy;              /* (b,L,H,P) dtype                                */
+  const float* dfinal_states;  /* like final_states, or NULL = 0; what is given
+                                  for ids that do not occur is not read          */
+  void* dq;                    /* (b,L,G,N) dtype, output                        */
+  void* dk;                    /* (b,L,G,N) dtype, output                        */
+  void* dv;                    /* (b,L,H,P) dtype, output                        */
+  float* dg;                   /* (b,L,H) fp32, output                           */
+  float* dbeta;                /* (b,L,H) fp32, output                           */
+  float* dinitial_states;      /* (b,H,P,N) fp32 output, or NULL to skip         */
+  void* workspace;             /* ssd_delta_bwd_workspace_size bytes, 256-byte
+                                  aligned; contents on entry do not matter       */
+  size_t workspace_bytes;
+} ssd_delta_bwd_args;
+
+/* Workspace bytes ssd_delta_bwd needs, or 0 if the sizes are invalid. */
+SSD_API size_t ssd_delta_bwd_workspace_size(const ssd_delta_bwd_args* args);
+
+SSD_API ssd_status ssd_delta_bwd(const ssd_delta_bwd_args* args, void* stream);
+
+/* Layer norm over the last axis with the block's gate: per row of cols values
+ *
+ *   y = ((x - mean) rstd weight + bias) SiLU(z),   rstd = (var + eps)^-1/2
+ *
+ * var the mean of (x - mean)^2, SiLU(z) = z / (1 + e^-z); weight, bias and the
+ * gate z each optional.  rows = b L H, cols = headdim normalises every head's
+ * output of the SSD or the delta rule; rows = b L the block's whole width.
+ * The pages' block names no norm; it has no counterpart there.  Any cols and
+ * rows below 2^31 each.  out may be x itself or z itself; else it must not
+ * overlap them.  Asynchronous on `stream`; nothing is enqueued when the
+ * arguments are rejected. */
+typedef struct {
+  int64_t rows, cols;
+  ssd_dtype dtype;      /* of x, z and out                          */
+  float eps;            /* >= 0                                     */
+  const void* x;        /* (rows,cols) dtype                        */
+  const float* weight;  /* (cols) fp32, or NULL for 1               */
+  const float* bias;    /* (cols) fp32, or NULL for 0               */
+  const void* z;        /* (rows,cols) dtype gate, or NULL for none */
+  void* out;            /* (rows,cols) dtype                        */
+} ssd_norm_args;
+
+SSD_API ssd_status ssd_layer_norm(const ssd_norm_args* args, void* stream);
+
+/* The backward of ssd_layer_norm: with n = (x - mean) rstd recomputed and
+ * h = dout SiLU(z) (dout without a gate), hw = h weight,
+ *
+ *   dx = rstd (hw - mean(hw) - n mean(hw n))     means over the row
+ *   dweight = sum over rows of h n,  dbias = sum over rows of h
+ *   dz = dout (n weight + bias) SiLU'(z)
+ *
+ * dx and dz in dtype, dweight and dbias fp32, summed in a fixed order, so
+ * results are deterministic.  dweight and dbias may be NULL to skip them;
+ * dz is required iff z.  Outputs must not overlap inputs or the workspace. */
+typedef struct {
+  int64_t rows, cols;
+  ssd_dtype dtype;      /* of x, z, dout, dx and dz                 */
+  float eps;
+  const void* x;
+  const float* weight;
+  const float* bias;
+  const void* z;
+  const void* dout;     /* (rows,cols) dtype, dLoss/dout            */
+  void* dx;             /* (rows,cols) dtype, output                */
+  float* dweight;       /* (cols) fp32 output, or NULL              */
+  float* dbias;         /* (cols) fp32 output, or NULL              */
+  void* dz;             /* (rows,cols) dtype output, iff z          */
+  void* workspace;      /* ssd_layer_norm_bwd_workspace_size bytes,
+                           256-byte aligned                         */
+  size_t workspace_bytes;
+} ssd_norm_bwd_args;
+
+/* Workspace bytes ssd_layer_norm_bwd needs (rows and cols only), or 0 if the
+ * sizes are invalid. */
+SSD_API size_t ssd_layer_norm_bwd_workspace_size(const ssd_norm_bwd_args* args);
+
+SSD_API ssd_status ssd_layer_norm_bwd(const ssd_norm_bwd_args* args, void* stream);
+
 /* The seq_idx precondition, on a HOST copy (b,L) int32: ids in [0, num_seqs),
  * non-decreasing along each row, and no id in two rows.  SSD_OK, or
  * SSD_ERR_INVALID_ARG at the first violation (or for a null pointer or a

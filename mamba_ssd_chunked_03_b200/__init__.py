@@ -13,6 +13,11 @@ fallback, and importing fails loudly if the library is missing.
     y_t = step(x_t, dt_t, A, B_t, C_t, D, state)   # one decode step, state in place
     grads = bwd(x, dt, A, B, C, D, dy)              # the backward (fp32 gradients)
     y, final_states = ssd_chunked(x, dt, A, B, C, D)  # differentiable: fwd, then bwd
+
+    y, final_states = delta_fwd(q, k, v, g, beta)    # the gated delta rule, its backward
+    grads = delta_bwd(q, k, v, g, beta, dy)          # (delta_chunked: differentiable) and
+    y_t = delta_step(q_t, k_t, v_t, g_t, beta_t, state)  # its decode step
+    out = layer_norm(y, weight, bias, z=z)           # the norm of the block's output, gated
 """
 from __future__ import annotations
 
@@ -22,7 +27,9 @@ from typing import Optional
 
 import torch
 
-__all__ = ["fwd", "fwd_host", "bwd", "BwdArgs", "bwd_workspace_size", "bwd_chunk_size", "bwd_path", "ssd_chunked", "make_args",
+__all__ = ["delta_fwd", "delta_bwd", "delta_chunked", "delta_step", "DeltaArgs", "DeltaBwdArgs", "DeltaStepArgs",
+           "layer_norm", "layer_norm_bwd", "gated_layer_norm", "NormArgs", "NormBwdArgs",
+           "fwd", "fwd_host", "bwd", "BwdArgs", "bwd_workspace_size", "bwd_chunk_size", "bwd_path", "ssd_chunked", "make_args",
            "make_bwd_args", "main_kernel", "device_status",
            "conv1d_silu_bwd", "ConvBwdArgs", "causal_conv1d_silu", "step", "StepArgs", "total_decay", "state_fold", "conv1d_silu", "ConvArgs", "workspace_size", "launch_count", "kernel_path", "SSDError", "lib", "LIB_PATH", "Args",
            "SSD_OK", "SSD_ERR_INVALID_ARG", "SSD_ERR_UNSUPPORTED", "SSD_ERR_WORKSPACE", "SSD_ERR_CUDA",
@@ -104,6 +111,56 @@ class ConvBwdArgs(ctypes.Structure):
     ]
 
 
+class DeltaArgs(ctypes.Structure):
+    """Mirror of ``ssd_delta_args``."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "nheads", "headdim", "dstate", "ngroups")] + [
+        ("dtype", ctypes.c_int),
+        ("flags", ctypes.c_uint32),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("g", ctypes.c_void_p), ("beta", ctypes.c_void_p),
+        ("initial_states", ctypes.c_void_p), ("seq_idx", ctypes.c_void_p),
+        ("num_seqs", ctypes.c_int64),
+        ("y", ctypes.c_void_p), ("final_states", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class DeltaBwdArgs(ctypes.Structure):
+    """Mirror of ``ssd_delta_bwd_args``."""
+    _fields_ = [("fwd", DeltaArgs)] + [(n, ctypes.c_void_p) for n in
+                ("dy", "dfinal_states", "dq", "dk", "dv", "dg", "dbeta", "dinitial_states", "workspace")] + [
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class DeltaStepArgs(ctypes.Structure):
+    """Mirror of ``ssd_delta_step_args``."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "nheads", "headdim", "dstate", "ngroups")] + [
+        ("dtype", ctypes.c_int),
+        ("scale", ctypes.c_float),
+    ] + [(n, ctypes.c_void_p) for n in ("q", "k", "v", "g", "beta", "state", "y")]
+
+
+class NormArgs(ctypes.Structure):
+    """Mirror of ``ssd_norm_args``."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "cols")] + [
+        ("dtype", ctypes.c_int),
+        ("eps", ctypes.c_float),
+    ] + [(n, ctypes.c_void_p) for n in ("x", "weight", "bias", "z", "out")]
+
+
+class NormBwdArgs(ctypes.Structure):
+    """Mirror of ``ssd_norm_bwd_args``."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "cols")] + [
+        ("dtype", ctypes.c_int),
+        ("eps", ctypes.c_float),
+    ] + [(n, ctypes.c_void_p) for n in
+         ("x", "weight", "bias", "z", "dout", "dx", "dweight", "dbias", "dz", "workspace")] + [
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -148,6 +205,14 @@ def _load() -> ctypes.CDLL:
     L.ssd_total_decay.restype = ctypes.c_int
     L.ssd_state_fold.argtypes = [ctypes.c_void_p] * 4 + [ctypes.c_int64] * 5 + [ctypes.c_void_p]
     L.ssd_state_fold.restype = ctypes.c_int
+    for name, args in (("ssd_delta_fwd", DeltaArgs), ("ssd_delta_bwd", DeltaBwdArgs), ("ssd_delta_step", DeltaStepArgs),
+                       ("ssd_layer_norm", NormArgs), ("ssd_layer_norm_bwd", NormBwdArgs)):
+        getattr(L, name).argtypes = [ctypes.POINTER(args), ctypes.c_void_p]
+        getattr(L, name).restype = ctypes.c_int
+    for name, args in (("ssd_delta_fwd_workspace_size", DeltaArgs), ("ssd_delta_bwd_workspace_size", DeltaBwdArgs),
+                       ("ssd_layer_norm_bwd_workspace_size", NormBwdArgs)):
+        getattr(L, name).argtypes = [ctypes.POINTER(args)]
+        getattr(L, name).restype = ctypes.c_size_t
     L.ssd_check_seq_idx.argtypes = [ctypes.c_void_p] + [ctypes.c_int64] * 3
     L.ssd_check_seq_idx.restype = ctypes.c_int
     L.ssd_status_string.argtypes = [ctypes.c_int]
@@ -727,3 +792,304 @@ def causal_conv1d_silu(u: torch.Tensor, weight: torch.Tensor, bias: Optional[tor
     """Differentiable ``conv1d_silu``: the backward runs ``ssd_conv1d_silu_bwd``
     (the pre-activation is recomputed, nothing but the inputs is kept)."""
     return _CausalConv1dSilu.apply(u, weight, bias, seq_idx)
+
+
+def _call(entry, args, device: torch.device) -> None:
+    """Run a library entry point on the current stream of ``device``, which is
+    made the current device for the call if it is not."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = entry(ctypes.byref(args), torch.cuda.current_stream(index).cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            st = entry(ctypes.byref(args), torch.cuda.current_stream(index).cuda_stream)
+    if st != SSD_OK:
+        raise SSDError(st)
+
+
+def _check_tensors(dev: torch.device, named) -> None:
+    if dev.type != "cuda":
+        raise ValueError("the tensors must be CUDA tensors")
+    for name, t in named:
+        if t is not None and (t.device != dev or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+
+
+def _check_delta(q, k, v, g, beta, initial_states, seq_idx):
+    if q.dim() != 4 or v.dim() != 4 or k.shape != q.shape:
+        raise ValueError("expected q and k (b,L,G,N), v (b,L,H,P), g and beta (b,L,H)")
+    b, L, H, P = v.shape
+    G, N = q.shape[2], q.shape[3]
+    if q.shape[0] != b or q.shape[1] != L or tuple(g.shape) != (b, L, H) or tuple(beta.shape) != (b, L, H):
+        raise ValueError("shapes do not match q and k (b,L,G,N), v (b,L,H,P), g and beta (b,L,H)")
+    if v.dtype not in (torch.float32, torch.bfloat16) or q.dtype != v.dtype or k.dtype != v.dtype:
+        raise TypeError("q, k and v must all be float32 or all bfloat16")
+    if g.dtype != torch.float32 or beta.dtype != torch.float32:
+        raise TypeError("g and beta must be float32")
+    if initial_states is not None and (initial_states.dtype != torch.float32
+                                       or tuple(initial_states.shape) != (b, H, P, N)):
+        raise ValueError("initial_states must be float32 (b, H, P, N)")
+    if seq_idx is not None and (seq_idx.dtype != torch.int32 or tuple(seq_idx.shape) != (b, L)):
+        raise ValueError("seq_idx must be int32 (b, L)")
+    _check_tensors(v.device, (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta),
+                              ("initial_states", initial_states), ("seq_idx", seq_idx)))
+
+
+def _fill_delta(a, q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs) -> None:
+    a.batch, a.seqlen, a.nheads, a.headdim = v.shape
+    a.ngroups, a.dstate = q.shape[2], q.shape[3]
+    a.dtype = SSD_BF16 if v.dtype == torch.bfloat16 else SSD_F32
+    a.q, a.k, a.v, a.g, a.beta = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr()
+    a.initial_states, a.seq_idx = _ptr(initial_states), _ptr(seq_idx)
+    a.num_seqs = int(num_seqs) if seq_idx is not None else 0
+    a.scale = float(a.dstate ** -0.5 if scale is None else scale)
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
+    """The caller's workspace if it is large enough, else a new one."""
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+        if workspace.numel() * workspace.element_size() >= need:
+            return workspace
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def _output(out: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return out
+
+
+def delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+              scale: Optional[float] = None, initial_states: Optional[torch.Tensor] = None,
+              seq_idx: Optional[torch.Tensor] = None, num_seqs: Optional[int] = None,
+              return_final_states: bool = True, y: Optional[torch.Tensor] = None,
+              final_states: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              check_seq: bool = False):
+    """The gated delta rule over whole sequences via ``ssd_delta_fwd``: per
+    head S_t = exp(g_t) S_{t-1} + u_t k_t^T with
+    u_t = beta_t (v_t - exp(g_t) S_{t-1} k_t), and y_t = scale S_t q_t.
+    Returns (y, final_states or None).
+
+    q and k (b,L,G,N) and v (b,L,H,P) fp32|bf16, g (log decay) and beta
+    (b,L,H) fp32; head h takes q and k of group h / (H / G).  ``scale``: N^-1/2
+    if None.  initial_states (b,H,P,N) fp32 or None; seq_idx (b,L) int32 or
+    None as for ``fwd`` (each id one run); with seq_idx, final_states is
+    (num_seqs,H,P,N), else (b,H,P,N).  ``y``, ``final_states`` and
+    ``workspace`` may be passed preallocated.  ``check_seq``: check the
+    seq_idx precondition on a host copy first (synchronous)."""
+    _check_delta(q, k, v, g, beta, initial_states, seq_idx)
+    b, L, H, P = v.shape
+    if seq_idx is not None and num_seqs is None:
+        num_seqs = int(seq_idx.max().item()) + 1
+    y = _output(y, "y", v.shape, v.dtype, v.device)
+    if return_final_states:
+        final_states = _output(final_states, "final_states",
+                               (num_seqs if seq_idx is not None else b, H, P, q.shape[3]), torch.float32, v.device)
+    else:
+        final_states = None
+    a = DeltaArgs()
+    _fill_delta(a, q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs)
+    a.flags = SSD_FLAG_CHECK_SEQ if check_seq else 0
+    a.y, a.final_states = y.data_ptr(), _ptr(final_states)
+    if seq_idx is not None:
+        need = int(lib.ssd_delta_fwd_workspace_size(ctypes.byref(a)))
+        if need:
+            workspace = _workspace(workspace, need, v.device)
+            a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call(lib.ssd_delta_fwd, a, v.device)
+    return y, final_states
+
+
+def delta_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+              dy: torch.Tensor, scale: Optional[float] = None, initial_states: Optional[torch.Tensor] = None,
+              seq_idx: Optional[torch.Tensor] = None, num_seqs: Optional[int] = None,
+              dfinal_states: Optional[torch.Tensor] = None, want_dinitial_states: Optional[bool] = None,
+              workspace: Optional[torch.Tensor] = None) -> dict:
+    """The backward of ``delta_fwd`` via ``ssd_delta_bwd``: gradients of a loss
+    given dy = dLoss/dy (like v) and dfinal_states = dLoss/dfinal_states (like
+    final_states, also with seq_idx, or None).  Returns a dict: dq, dk and dv
+    in their inputs' dtype, dg, dbeta and dinitial_states (by default only
+    when initial_states is given, else None) fp32."""
+    _check_delta(q, k, v, g, beta, initial_states, seq_idx)
+    b, L, H, P = v.shape
+    N = q.shape[3]
+    if seq_idx is not None and num_seqs is None:
+        num_seqs = int(seq_idx.max().item()) + 1
+    if dy.dtype != v.dtype or dy.shape != v.shape:
+        raise ValueError("dy must be like v")
+    rows = num_seqs if seq_idx is not None else b
+    if dfinal_states is not None and (dfinal_states.dtype != torch.float32
+                                      or tuple(dfinal_states.shape) != (rows, H, P, N)):
+        raise ValueError(f"dfinal_states must be float32 {(rows, H, P, N)}")
+    _check_tensors(v.device, (("dy", dy), ("dfinal_states", dfinal_states)))
+    if want_dinitial_states is None:
+        want_dinitial_states = initial_states is not None
+    d = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v), "dg": torch.empty_like(g),
+         "dbeta": torch.empty_like(beta),
+         "dinitial_states": torch.empty(b, H, P, N, device=v.device, dtype=torch.float32)
+         if want_dinitial_states else None}
+    a = DeltaBwdArgs()
+    _fill_delta(a.fwd, q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs)
+    a.dy, a.dfinal_states = dy.data_ptr(), _ptr(dfinal_states)
+    a.dq, a.dk, a.dv, a.dg, a.dbeta, a.dinitial_states = (_ptr(d[n]) for n in (
+        "dq", "dk", "dv", "dg", "dbeta", "dinitial_states"))
+    need = int(lib.ssd_delta_bwd_workspace_size(ctypes.byref(a)))
+    if need:
+        workspace = _workspace(workspace, need, v.device)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call(lib.ssd_delta_bwd, a, v.device)
+    return d
+
+
+class _DeltaChunked(torch.autograd.Function):
+    """``delta_fwd`` forward, ``delta_bwd`` backward."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs):
+        ctx.set_materialize_grads(False)
+        y, fin = delta_fwd(q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs)
+        ctx.save_for_backward(q, k, v, g, beta, initial_states, seq_idx)
+        ctx.scale, ctx.num_seqs = scale, num_seqs
+        return y, fin
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dfin):
+        q, k, v, g, beta, h0, seq = ctx.saved_tensors
+        dy = torch.zeros_like(v) if dy is None else dy.to(v.dtype).contiguous()
+        dfin = None if dfin is None else dfin.to(torch.float32).contiguous()
+        d = delta_bwd(q, k, v, g, beta, dy, ctx.scale, h0, seq, ctx.num_seqs, dfin,
+                      want_dinitial_states=h0 is not None and ctx.needs_input_grad[6])
+        return d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"], None, d["dinitial_states"], None, None
+
+
+def delta_chunked(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                  scale: Optional[float] = None, initial_states: Optional[torch.Tensor] = None,
+                  seq_idx: Optional[torch.Tensor] = None, num_seqs: Optional[int] = None):
+    """Differentiable ``delta_fwd``: returns (y, final_states), and its
+    backward runs ``delta_bwd`` (the states are recomputed, nothing but the
+    inputs is kept).  Gradients through the final states are taken, with
+    seq_idx too."""
+    if seq_idx is not None and num_seqs is None:
+        num_seqs = int(seq_idx.max().item()) + 1
+    return _DeltaChunked.apply(q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs)
+
+
+def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+               state: torch.Tensor, scale: Optional[float] = None, y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of the gated delta rule (decode) via ``ssd_delta_step``: q and
+    k (b,G,N), v (b,H,P), g and beta (b,H) fp32, state (b,H,P,N) fp32, updated
+    in place.  ``scale``: N^-1/2 if None.  Returns y (b,H,P) in v's dtype."""
+    if q.dim() != 3 or v.dim() != 3 or k.shape != q.shape:
+        raise ValueError("expected q and k (b,G,N), v (b,H,P), g and beta (b,H), state (b,H,P,N)")
+    b, H, P = v.shape
+    G, N = q.shape[1], q.shape[2]
+    if q.shape[0] != b or tuple(g.shape) != (b, H) or tuple(beta.shape) != (b, H) or tuple(state.shape) != (b, H, P, N):
+        raise ValueError("shapes do not match q and k (b,G,N), v (b,H,P), g and beta (b,H), state (b,H,P,N)")
+    if v.dtype not in (torch.float32, torch.bfloat16) or q.dtype != v.dtype or k.dtype != v.dtype:
+        raise TypeError("q, k and v must all be float32 or all bfloat16")
+    if g.dtype != torch.float32 or beta.dtype != torch.float32 or state.dtype != torch.float32:
+        raise TypeError("g, beta and state must be float32")
+    _check_tensors(v.device, (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("state", state)))
+    y = _output(y, "y", v.shape, v.dtype, v.device)
+    a = DeltaStepArgs()
+    a.batch, a.nheads, a.headdim, a.dstate, a.ngroups = b, H, P, N, G
+    a.dtype = SSD_BF16 if v.dtype == torch.bfloat16 else SSD_F32
+    a.scale = float(N ** -0.5 if scale is None else scale)
+    a.q, a.k, a.v, a.g, a.beta = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr()
+    a.state, a.y = state.data_ptr(), y.data_ptr()
+    _call(lib.ssd_delta_step, a, v.device)
+    return y
+
+
+def _check_norm(x, weight, bias, z) -> None:
+    if x.dim() < 1:
+        raise ValueError("x must have at least one axis")
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("x must be float32 or bfloat16")
+    cols = x.shape[-1]
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (cols,)):
+            raise ValueError(f"{name} must be float32 ({cols},)")
+    if z is not None and (z.dtype != x.dtype or z.shape != x.shape):
+        raise ValueError("z must be like x")
+    _check_tensors(x.device, (("x", x), ("weight", weight), ("bias", bias), ("z", z)))
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, z: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``ssd_layer_norm``: ((x - mean) rstd weight + bias) SiLU(z) over the last
+    axis of x (..., D) fp32|bf16, weight and bias (D) fp32 or None, the gate z
+    like x or None (then without SiLU(z)).  ``out`` may be x or z itself."""
+    _check_norm(x, weight, bias, z)
+    out = _output(out, "out", x.shape, x.dtype, x.device)
+    a = NormArgs()
+    a.cols = x.shape[-1]
+    a.rows = x.numel() // a.cols if a.cols else 0
+    a.dtype = SSD_BF16 if x.dtype == torch.bfloat16 else SSD_F32
+    a.eps = eps
+    a.x, a.weight, a.bias, a.z, a.out = x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(z), out.data_ptr()
+    _call(lib.ssd_layer_norm, a, x.device)
+    return out
+
+
+def layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor], dout: torch.Tensor,
+                   eps: float = 1e-5, z: Optional[torch.Tensor] = None, want_dweight: Optional[bool] = None,
+                   want_dbias: Optional[bool] = None) -> tuple:
+    """``ssd_layer_norm_bwd``: (dx, dweight, dbias, dz) for
+    dout = dLoss/d(layer_norm(x, weight, bias, eps, z)).  dx and dz (None
+    without a gate) in x's dtype; dweight and dbias fp32, by default where
+    weight and bias are given, else None."""
+    _check_norm(x, weight, bias, z)
+    if dout.dtype != x.dtype or dout.shape != x.shape:
+        raise ValueError("dout must be like x")
+    _check_tensors(x.device, (("dout", dout),))
+    cols = x.shape[-1]
+    want_dweight = weight is not None if want_dweight is None else want_dweight
+    want_dbias = bias is not None if want_dbias is None else want_dbias
+    dx = torch.empty_like(x)
+    dw = torch.empty(cols, device=x.device, dtype=torch.float32) if want_dweight else None
+    db = torch.empty(cols, device=x.device, dtype=torch.float32) if want_dbias else None
+    dz = torch.empty_like(x) if z is not None else None
+    a = NormBwdArgs()
+    a.cols = cols
+    a.rows = x.numel() // cols if cols else 0
+    a.dtype = SSD_BF16 if x.dtype == torch.bfloat16 else SSD_F32
+    a.eps = eps
+    a.x, a.weight, a.bias, a.z, a.dout = x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(z), dout.data_ptr()
+    a.dx, a.dweight, a.dbias, a.dz = dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(dz)
+    need = int(lib.ssd_layer_norm_bwd_workspace_size(ctypes.byref(a)))
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), need
+    _call(lib.ssd_layer_norm_bwd, a, x.device)
+    return dx, dw, db, dz
+
+
+class _GatedLayerNorm(torch.autograd.Function):
+    """``layer_norm`` forward, ``layer_norm_bwd`` backward."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, z):
+        ctx.save_for_backward(x, weight, bias, z)
+        ctx.eps = eps
+        return layer_norm(x, weight, bias, eps, z)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        x, weight, bias, z = ctx.saved_tensors
+        dx, dw, db, dz = layer_norm_bwd(x, weight, bias, dout.to(x.dtype).contiguous(), ctx.eps, z,
+                                        want_dweight=weight is not None and ctx.needs_input_grad[1],
+                                        want_dbias=bias is not None and ctx.needs_input_grad[2])
+        return dx, dw, db, None, dz
+
+
+def gated_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                     eps: float = 1e-5, z: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Differentiable ``layer_norm``: the backward runs ``ssd_layer_norm_bwd``
+    (the statistics are recomputed, nothing but the inputs is kept)."""
+    return _GatedLayerNorm.apply(x, weight, bias, eps, z)

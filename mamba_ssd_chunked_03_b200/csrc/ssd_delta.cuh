@@ -1,0 +1,141 @@
+// Shared pieces of the gated delta rule's kernels (ssd_delta_fwd.cu,
+// ssd_delta_bwd.cu): the run list, the warp-level matrix instruction, and the
+// operand split that keeps fp32 accuracy on 16-bit matrix instructions.
+//
+// Operands.  Every matrix operand is held as fp16 after its rows have been
+// brought to [2^14, 2^15) by a power of two that is folded back into the fp32
+// result (pow2_scale).  A bf16 row is then exact in one term (8 bits, down to
+// 2^-28 of its row's largest value); an fp32 row is split in two, hi + lo with
+// 11 bits each, so that a product of an exact and a split operand takes two
+// instructions and is off by about 2^-22, and one of two split operands takes
+// three (lo * lo is left out: 2^-22 again).  bf16 terms would need three and
+// six for the same accuracy.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "sm100.cuh"
+#include "ssd.h"
+
+namespace ssd {
+namespace delta {
+
+constexpr int kC = 32;         // tokens of a chunk
+constexpr int kCheck = 64;     // tokens between two state checkpoints of the backward
+
+// One sequence: a row without seq_idx, or one run of equal ids.
+struct Run {
+  int64_t tok;   // first token, counted over all rows (row * L + t)
+  int64_t slot;  // first checkpoint (64 tokens each)
+  int32_t len;   // tokens; 0: an id that does not occur (its final state is zeroed)
+  int32_t fin;   // index of its final state
+  int32_t h0;    // row whose initial state it starts from, or -1
+  int32_t pad;
+};
+
+// ---------------------------------------------------------------- elements
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// The power of two that brings a row with largest magnitude m to [2^14, 2^15),
+// and its inverse (m = 0, denormal, infinite or NaN: the nearest that exists).
+__device__ __forceinline__ float pow2_scale(float m, float& inv) {
+  int e = (int)(__float_as_uint(m) >> 23);
+  e = e < 15 ? 15 : e > 253 ? 253 : e;
+  inv = __uint_as_float((uint32_t)(e - 14) << 23);
+  return __uint_as_float((uint32_t)(268 - e) << 23);
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+// hi and lo terms of two scaled values
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack2(a, b);
+  const float2 f = unpack2(hi);
+  lo = pack2(a - f.x, b - f.y);
+}
+
+// ---------------------------------------------------------------- matrix instruction
+// D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16).  Thread i of the
+// warp holds D at rows i/4 and i/4 + 8, columns 2(i%4) and 2(i%4) + 1; A at
+// the same rows and columns (registers 0, 1: columns 0-7; 2, 3: 8-15); B at
+// column i/4, rows 2(i%4).. and 2(i%4) + 8...  So a D tile pair is an A tile
+// as it stands, and a product can be fed to the next without leaving the
+// registers.
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) { sm100::ldmatrix_x4_trans(addr, r); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;  // 0: the 16 bytes are zeros and nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Byte offset of (row, column) in a tile of fp16 rows: W columns each, the
+// 16-byte pieces of a row permuted by its index so that the eight rows of an
+// ldmatrix lie in different banks.
+template <int W>
+__device__ __forceinline__ uint32_t tile_off(int row, int col) {
+  if constexpr (W == 32)
+    return (uint32_t)(row * 64 + (((col >> 3) ^ ((row >> 1) & 3)) << 4) + (col & 7) * 2);
+  else
+    return (uint32_t)(row * (W * 2) + (((col >> 3) ^ (row & 7)) << 4) + (col & 7) * 2);
+}
+
+// The largest magnitude over the four threads that share a row of D.
+__device__ __forceinline__ float quad_max(float m) {
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+}
+// The largest magnitude over the warp (the bits of a non-negative float order as it does).
+__device__ __forceinline__ float warp_absmax(float m) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
+
+// g, bounded below where exp is zero anyway: a decay of -inf (a reset) then
+// leaves the cumulative sums finite.  NaN stays NaN.
+__device__ __forceinline__ double decay_log(float g) { return g < -1.0e4f ? -1.0e4 : (double)g; }
+
+struct Shape {
+  int64_t b, L, H, G, P, N, num_seqs;
+  int64_t runs;   // units of the run list
+  int64_t slots;  // checkpoints over all runs
+  bool bf16, packed;
+};
+
+size_t runs_bytes(const Shape& s);
+// SSD_FLAG_CHECK_SEQ: the precondition on a host copy of seq (waits for `stream`).
+ssd_status check_seq_device(const int32_t* seq, int64_t b, int64_t L, int64_t num_seqs, cudaStream_t stream);
+// Enqueue the run list of seq_idx (packed) into ws: `runs` entries, longest
+// first, ids that do not occur as runs of length 0 after them.
+cudaError_t launch_runs(const Shape& s, const int32_t* seq, void* ws, cudaStream_t stream);
+
+}  // namespace delta
+}  // namespace ssd

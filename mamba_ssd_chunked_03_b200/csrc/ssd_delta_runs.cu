@@ -1,0 +1,139 @@
+// The run list of packed sequences for the gated delta rule: one CTA finds
+// where the id changes, counts and ranks the runs (longest first, so that the
+// last CTAs to start are short), and lists the ids that do not occur, whose
+// final states the main kernel zeroes.
+//
+// Bound by latency: the ids are read twice, 32 at a time per warp with eight
+// loads in flight, each warp over its own contiguous range.  16384 ids take
+// about 8 us.
+#include <vector>
+
+#include "ssd_delta.cuh"
+#include "ssd_internal.h"
+
+namespace ssd {
+namespace delta {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kRanked = 2048;  // runs up to which they are ranked (quadratic work)
+
+__device__ __forceinline__ bool starts(const int32_t* seq, int64_t i, int64_t L) {
+  return i % L == 0 || seq[i] != seq[i - 1];
+}
+
+__global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restrict__ seq, int64_t n, int64_t L,
+                                                         int64_t cap, Run* runs, int32_t* first, int32_t* present) {
+  __shared__ int warp_count[32];
+  __shared__ int total, absent;
+  __shared__ int lens[kRanked];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t i = threadIdx.x; i < cap; i += kThreads) {
+    present[i] = 0;
+    Run r = {};
+    r.fin = r.h0 = -1;
+    runs[i] = r;
+  }
+  const int64_t per = ((n + 31) / 32 + 31) / 32 * 32;  // ids per warp, a multiple of 32
+  const int64_t i0 = warp * per, i1 = i0 + per < n ? i0 + per : n;
+  int count = 0;
+  for (int64_t i = i0; i < i1; i += 256) {
+    bool s[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s[u] = i + 32 * u + lane < i1 && starts(seq, i + 32 * u + lane, L);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) count += __popc(__ballot_sync(0xffffffffu, s[u]));
+  }
+  if (lane == 0) warp_count[warp] = count;
+  if (threadIdx.x == 0) absent = 0;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int sum = 0;
+    for (int w = 0; w < 32; ++w) {
+      const int c = warp_count[w];
+      warp_count[w] = sum;
+      sum += c;
+    }
+    total = sum;
+  }
+  __syncthreads();
+  int64_t at = warp_count[warp];
+  for (int64_t i = i0; i < i1; i += 256) {
+    bool s[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s[u] = i + 32 * u + lane < i1 && starts(seq, i + 32 * u + lane, L);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t m = __ballot_sync(0xffffffffu, s[u]);
+      const int64_t k = at + __popc(m & ((1u << lane) - 1u));
+      if (s[u] && k <= cap) first[k] = (int32_t)(i + 32 * u + lane);
+      at += __popc(m);
+    }
+  }
+  __syncthreads();
+  // more runs than num_seqs (ids that come back): the rest is left out
+  const int64_t nr = total < cap ? total : cap;
+  const auto len_of = [&](int64_t k) { return (int)((k + 1 < total ? first[k + 1] : n) - first[k]); };
+  const bool ranked = nr <= kRanked;
+  if (ranked) {
+    for (int64_t k = threadIdx.x; k < nr; k += kThreads) lens[k] = len_of(k);
+    __syncthreads();
+  }
+  for (int64_t k = threadIdx.x; k < nr; k += kThreads) {
+    const int64_t t = first[k];
+    const int id = seq[t], len = ranked ? lens[k] : len_of(k);
+    int64_t rank = k;
+    if (ranked) {
+      rank = 0;
+      for (int j = 0; j < nr; ++j) rank += lens[j] > len || (lens[j] == len && j < k);
+    }
+    Run r;
+    r.tok = t;
+    r.slot = t / kCheck + k;
+    r.len = len;
+    r.fin = id >= 0 && id < cap ? id : -1;
+    r.h0 = t % L == 0 ? (int32_t)(t / L) : -1;
+    r.pad = 0;
+    runs[rank] = r;
+    if (r.fin >= 0) present[r.fin] = 1;
+  }
+  __syncthreads();
+  for (int64_t i = threadIdx.x; i < cap; i += kThreads) {
+    if (present[i]) continue;
+    const int64_t k = nr + atomicAdd(&absent, 1);  // any order: each of them writes zeros
+    if (k < cap) runs[k].fin = (int32_t)i;
+  }
+}
+
+}  // namespace
+
+size_t runs_bytes(const Shape& s) {
+  return s.packed ? align_up((size_t)s.num_seqs * sizeof(Run), kWsAlign) + 2 * align_up((size_t)(s.num_seqs + 1) * 4, kWsAlign)
+                  : 0;
+}
+
+cudaError_t launch_runs(const Shape& s, const int32_t* seq, void* ws, cudaStream_t stream) {
+  char* p = static_cast<char*>(ws);
+  Run* runs = reinterpret_cast<Run*>(p);
+  p += align_up((size_t)s.num_seqs * sizeof(Run), kWsAlign);
+  int32_t* first = reinterpret_cast<int32_t*>(p);
+  p += align_up((size_t)(s.num_seqs + 1) * 4, kWsAlign);
+  k_delta_runs<<<1, kThreads, 0, stream>>>(seq, s.b * s.L, s.L, s.num_seqs, runs, first, reinterpret_cast<int32_t*>(p));
+  return cudaGetLastError();
+}
+
+ssd_status check_seq_device(const int32_t* seq, int64_t b, int64_t L, int64_t num_seqs, cudaStream_t stream) {
+  try {
+    std::vector<int32_t> host((size_t)(b * L));
+    if (cudaMemcpyAsync(host.data(), seq, host.size() * sizeof(int32_t), cudaMemcpyDeviceToHost, stream) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess)
+      return SSD_ERR_CUDA;
+    return ssd_check_seq_idx(host.data(), b, L, num_seqs);
+  } catch (...) {  // no host memory for the copy
+    return SSD_ERR_UNSUPPORTED;
+  }
+}
+
+}  // namespace delta
+}  // namespace ssd

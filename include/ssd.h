@@ -527,17 +527,16 @@ typedef struct {
   float* final_states;         /* output or NULL: (b,H,P,N) fp32; with seq_idx
                                   (num_seqs,H,P,N), zeros for absent ids         */
   void* workspace;             /* ssd_delta_fwd_workspace_size bytes, 256-byte
-                                  aligned (NULL when that is 0); contents on
-                                  entry do not matter                            */
+                                  aligned; contents on entry do not matter       */
   size_t workspace_bytes;
   float scale;                 /* of y; dstate^-1/2 is usual                     */
 } ssd_delta_args;
 
 /* Workspace bytes ssd_delta_fwd needs (sizes, dtype and the presence of
- * seq_idx only; 0 without seq_idx, or if the sizes are invalid). */
+ * seq_idx only), or 0 if the sizes are invalid. */
 SSD_API size_t ssd_delta_fwd_workspace_size(const ssd_delta_args* args);
 
-/* Enqueue the forward on `stream`: one kernel, and one before it with
+/* Enqueue the forward on `stream`: two kernels, and one before them with
  * seq_idx.  SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_WORKSPACE as
  * for ssd_fwd, with nothing enqueued; SSD_ERR_CUDA when a launch fails.
  * Outputs must not overlap the inputs. */

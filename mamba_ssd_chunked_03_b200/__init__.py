@@ -895,11 +895,10 @@ def delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
     _fill_delta(a, q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs)
     a.flags = SSD_FLAG_CHECK_SEQ if check_seq else 0
     a.y, a.final_states = y.data_ptr(), _ptr(final_states)
-    if seq_idx is not None:
-        need = int(lib.ssd_delta_fwd_workspace_size(ctypes.byref(a)))
-        if need:
-            workspace = _workspace(workspace, need, v.device)
-            a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    need = int(lib.ssd_delta_fwd_workspace_size(ctypes.byref(a)))
+    if need:
+        workspace = _workspace(workspace, need, v.device)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _call(lib.ssd_delta_fwd, a, v.device)
     return y, final_states
 

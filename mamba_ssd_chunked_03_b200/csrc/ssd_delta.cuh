@@ -2,14 +2,14 @@
 // ssd_delta_bwd.cu): the run list, the warp-level matrix instruction, and the
 // operand split that keeps fp32 accuracy on 16-bit matrix instructions.
 //
-// Operands.  Every matrix operand is held as fp16 after its rows have been
-// brought to [2^14, 2^15) by a power of two that is folded back into the fp32
-// result (pow2_scale).  A bf16 row is then exact in one term (8 bits, down to
-// 2^-28 of its row's largest value); an fp32 row is split in two, hi + lo with
-// 11 bits each, so that a product of an exact and a split operand takes two
-// instructions and is off by about 2^-22, and one of two split operands takes
-// three (lo * lo is left out: 2^-22 again).  bf16 terms would need three and
-// six for the same accuracy.
+// Operands.  Every matrix operand is held as fp16 after its rows (for the
+// tiles of q, k and the inverse: the tile) have been brought to [2^14, 2^15) by a power of
+// two that is folded back into the fp32 result (pow2_scale).  A bf16 value is
+// then exact in one term (8 bits, down to 2^-28 of the largest); an fp32 one
+// is split in two, hi + lo with 11 bits each, so that a product of an exact
+// and a split operand takes two instructions and is off by about 2^-22, and
+// one of two split operands takes three (lo * lo is left out: 2^-22 again).
+// bf16 terms would need three and six for the same accuracy.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -28,12 +28,18 @@ constexpr int kCheck = 64;     // tokens between two state checkpoints of the ba
 
 // One sequence: a row without seq_idx, or one run of equal ids.
 struct Run {
-  int64_t tok;   // first token, counted over all rows (row * L + t)
-  int64_t slot;  // first checkpoint (64 tokens each)
-  int32_t len;   // tokens; 0: an id that does not occur (its final state is zeroed)
-  int32_t fin;   // index of its final state
-  int32_t h0;    // row whose initial state it starts from, or -1
+  int64_t tok;    // first token, counted over all rows (row * L + t)
+  int64_t chunk;  // index of its first chunk among all runs' chunks
+  int64_t slot;   // index of its first checkpoint
+  int32_t len;    // tokens; 0: an id that does not occur (its final state is zeroed)
+  int32_t fin;    // index of its final state, or -1
+  int32_t h0;     // row whose initial state it starts from, or -1
   int32_t pad;
+};
+// A chunk's place: its first token over all rows, and how many of its 32
+// tokens exist (0: no such chunk).
+struct Chunk {
+  int32_t tok, n;
 };
 
 // ---------------------------------------------------------------- elements
@@ -55,17 +61,20 @@ __device__ __forceinline__ float pow2_scale(float m, float& inv) {
   return __uint_as_float((uint32_t)(268 - e) << 23);
 }
 
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+  const __half2 h = __float22half2_rn(v);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float2 unpack2(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
-// hi and lo terms of two scaled values
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pack2(a, b);
-  const float2 f = unpack2(hi);
-  lo = pack2(a - f.x, b - f.y);
+__device__ __forceinline__ float2 bf16x2(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
+// hi and lo terms of two scaled values
+__device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
+  hi = pack2(v);
+  lo = pack2(__ffma2_rn(unpack2(hi), make_float2(-1.f, -1.f), v));
+}
+__device__ __forceinline__ float2 mul2(float a, float b, float s) { return __fmul2_rn(make_float2(a, b), make_float2(s, s)); }
 
 // ---------------------------------------------------------------- matrix instruction
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16).  Thread i of the
@@ -114,28 +123,55 @@ __device__ __forceinline__ float quad_max(float m) {
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
   return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
-// The largest magnitude over the warp (the bits of a non-negative float order as it does).
-__device__ __forceinline__ float warp_absmax(float m) {
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+
+// g in powers of two, bounded below where its exponential is zero anyway: a
+// decay of -inf (a reset) then leaves the cumulative sums finite.  NaN stays NaN.
+__device__ __forceinline__ double decay_log2(float g) {
+  return (g < -1.0e4f ? -1.0e4 : (double)g) * 1.4426950408889634074;
 }
 
-// g, bounded below where exp is zero anyway: a decay of -inf (a reset) then
-// leaves the cumulative sums finite.  NaN stays NaN.
-__device__ __forceinline__ double decay_log(float g) { return g < -1.0e4f ? -1.0e4 : (double)g; }
+// 2^c, accurate to fp32 for any c (the fraction is taken in 64 bits).
+__device__ __forceinline__ float pow2_of(double c) {
+  const double i = rint(c);
+  return exp2f((float)(c - i)) * exp2f((float)i);
+}
 
 struct Shape {
   int64_t b, L, H, G, P, N, num_seqs;
-  int64_t runs;   // units of the run list
-  int64_t slots;  // checkpoints over all runs
+  int64_t runs;    // units of the run list
+  int64_t chunks;  // places of chunks over all runs
+  int64_t slots;   // places of checkpoints over all runs
   bool bf16, packed;
+  float scale;
 };
 
+// A run without a list: row `ri`.
+__device__ __forceinline__ Run row_run(int64_t ri, int64_t L) {
+  Run r;
+  r.tok = ri * L, r.len = (int32_t)L, r.fin = r.h0 = (int32_t)ri, r.pad = 0;
+  r.chunk = ri * ((L + kC - 1) / kC), r.slot = ri * ((L + kCheck - 1) / kCheck);
+  return r;
+}
+
+// The run list's part of the workspace: runs, chunks, and scratch.
+struct RunList {
+  Run* runs;
+  Chunk* chunks;
+  int32_t* first;
+  int32_t* present;
+};
 size_t runs_bytes(const Shape& s);
+RunList runs_at(const Shape& s, void* ws);
 // SSD_FLAG_CHECK_SEQ: the precondition on a host copy of seq (waits for `stream`).
 ssd_status check_seq_device(const int32_t* seq, int64_t b, int64_t L, int64_t num_seqs, cudaStream_t stream);
-// Enqueue the run list of seq_idx (packed) into ws: `runs` entries, longest
-// first, ids that do not occur as runs of length 0 after them.
-cudaError_t launch_runs(const Shape& s, const int32_t* seq, void* ws, cudaStream_t stream);
+// Enqueue the run list of seq_idx: `s.runs` entries, longest first, ids that
+// do not occur as runs of length 0 after them; and the places of the chunks.
+cudaError_t launch_runs(const Shape& s, const int32_t* seq, const RunList& r, cudaStream_t stream);
+
+// The sizes and options of a call, checked; SSD_OK, or why not.
+ssd_status resolve(const ssd_delta_args* a, Shape* s);
+
+inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 }  // namespace delta
 }  // namespace ssd

@@ -23,7 +23,8 @@ __device__ __forceinline__ bool starts(const int32_t* seq, int64_t i, int64_t L)
 }
 
 __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restrict__ seq, int64_t n, int64_t L,
-                                                         int64_t cap, Run* runs, int32_t* first, int32_t* present) {
+                                                         int64_t cap, int64_t places, Run* runs, Chunk* chunks,
+                                                         int32_t* first, int32_t* present) {
   __shared__ int warp_count[32];
   __shared__ int total, absent;
   __shared__ int lens[kRanked];
@@ -34,6 +35,7 @@ __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restri
     r.fin = r.h0 = -1;
     runs[i] = r;
   }
+  for (int64_t i = threadIdx.x; i < places; i += kThreads) chunks[i] = Chunk{0, 0};
   const int64_t per = ((n + 31) / 32 + 31) / 32 * 32;  // ids per warp, a multiple of 32
   const int64_t i0 = warp * per, i1 = i0 + per < n ? i0 + per : n;
   int count = 0;
@@ -89,6 +91,7 @@ __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restri
     }
     Run r;
     r.tok = t;
+    r.chunk = t / kC + k;  // at least as many places as the runs before it have chunks
     r.slot = t / kCheck + k;
     r.len = len;
     r.fin = id >= 0 && id < cap ? id : -1;
@@ -96,6 +99,11 @@ __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restri
     r.pad = 0;
     runs[rank] = r;
     if (r.fin >= 0) present[r.fin] = 1;
+  }
+  for (int64_t k = warp; k < nr; k += 32) {
+    const int t = first[k], len = ranked ? lens[k] : len_of(k);
+    for (int i = lane * kC; i < len; i += 32 * kC)
+      chunks[t / kC + k + i / kC] = Chunk{t + i, len - i < kC ? len - i : kC};
   }
   __syncthreads();
   for (int64_t i = threadIdx.x; i < cap; i += kThreads) {
@@ -108,17 +116,27 @@ __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restri
 }  // namespace
 
 size_t runs_bytes(const Shape& s) {
-  return s.packed ? align_up((size_t)s.num_seqs * sizeof(Run), kWsAlign) + 2 * align_up((size_t)(s.num_seqs + 1) * 4, kWsAlign)
-                  : 0;
+  if (!s.packed) return 0;
+  return align_up((size_t)s.runs * sizeof(Run), kWsAlign) + align_up((size_t)s.chunks * sizeof(Chunk), kWsAlign) +
+         2 * align_up((size_t)(s.runs + 1) * 4, kWsAlign);
 }
 
-cudaError_t launch_runs(const Shape& s, const int32_t* seq, void* ws, cudaStream_t stream) {
+RunList runs_at(const Shape& s, void* ws) {
+  if (!s.packed) return RunList{};
   char* p = static_cast<char*>(ws);
-  Run* runs = reinterpret_cast<Run*>(p);
-  p += align_up((size_t)s.num_seqs * sizeof(Run), kWsAlign);
-  int32_t* first = reinterpret_cast<int32_t*>(p);
-  p += align_up((size_t)(s.num_seqs + 1) * 4, kWsAlign);
-  k_delta_runs<<<1, kThreads, 0, stream>>>(seq, s.b * s.L, s.L, s.num_seqs, runs, first, reinterpret_cast<int32_t*>(p));
+  RunList r;
+  r.runs = reinterpret_cast<Run*>(p);
+  p += align_up((size_t)s.runs * sizeof(Run), kWsAlign);
+  r.chunks = reinterpret_cast<Chunk*>(p);
+  p += align_up((size_t)s.chunks * sizeof(Chunk), kWsAlign);
+  r.first = reinterpret_cast<int32_t*>(p);
+  p += align_up((size_t)(s.runs + 1) * 4, kWsAlign);
+  r.present = reinterpret_cast<int32_t*>(p);
+  return r;
+}
+
+cudaError_t launch_runs(const Shape& s, const int32_t* seq, const RunList& r, cudaStream_t stream) {
+  k_delta_runs<<<1, kThreads, 0, stream>>>(seq, s.b * s.L, s.L, s.runs, s.chunks, r.runs, r.chunks, r.first, r.present);
   return cudaGetLastError();
 }
 
@@ -133,6 +151,29 @@ ssd_status check_seq_device(const int32_t* seq, int64_t b, int64_t L, int64_t nu
   } catch (...) {  // no host memory for the copy
     return SSD_ERR_UNSUPPORTED;
   }
+}
+
+ssd_status resolve(const ssd_delta_args* a, Shape* s) {
+  if (!a || a->batch <= 0 || a->seqlen <= 0 || a->nheads <= 0 || a->headdim <= 0 || a->dstate <= 0 || a->ngroups <= 0)
+    return SSD_ERR_INVALID_ARG;
+  if (a->nheads % a->ngroups != 0 || (a->dtype != SSD_F32 && a->dtype != SSD_BF16)) return SSD_ERR_INVALID_ARG;
+  if (a->flags & ~SSD_FLAG_CHECK_SEQ) return SSD_ERR_INVALID_ARG;
+  if (a->seq_idx && a->num_seqs <= 0) return SSD_ERR_INVALID_ARG;
+  const double most = 2147483647.0, b = (double)a->batch, L = (double)a->seqlen, H = (double)a->nheads;
+  const double runs = a->seq_idx ? (double)a->num_seqs : b;
+  if (a->dstate > 256 || a->headdim > 65536) return SSD_ERR_UNSUPPORTED;
+  // grids (heads of chunks, 32-row slices of runs) and token counts below 2^31
+  if (b * L >= most || runs >= most || runs * H * (double)((a->headdim + 31) / 32) >= most ||
+      (b * (L / kC + 1) + runs) * H >= most)
+    return SSD_ERR_UNSUPPORTED;
+  s->b = a->batch, s->L = a->seqlen, s->H = a->nheads, s->G = a->ngroups, s->P = a->headdim, s->N = a->dstate;
+  s->packed = a->seq_idx != nullptr, s->bf16 = a->dtype == SSD_BF16, s->scale = a->scale;
+  s->num_seqs = s->packed ? a->num_seqs : 0;
+  s->runs = s->packed ? a->num_seqs : a->batch;
+  const int64_t tokens = s->b * s->L;
+  s->chunks = s->packed ? tokens / kC + s->runs : s->b * ((s->L + kC - 1) / kC);
+  s->slots = s->packed ? tokens / kCheck + s->runs : s->b * ((s->L + kCheck - 1) / kCheck);
+  return SSD_OK;
 }
 
 }  // namespace delta

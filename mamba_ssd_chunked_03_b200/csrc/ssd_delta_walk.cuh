@@ -1,20 +1,89 @@
-// The forward walk of the gated delta rule (see ssd_delta_core.cuh for the
+// The forward walk of the gated delta rule (ssd_delta_prep.cuh has the
 // formulas): one CTA carries 64 rows (headdim) of one head's state through one
 // sequence, 32 tokens at a time.
 //
-// Each of four state warps owns 16 rows p of the state for all N columns, in
+// Each of its four warps owns 16 rows p of the state for all N columns, in
 // registers, as the accumulator tiles of the matrix instruction.  Every
 // product of a chunk has m = p, so the result of one is the operand of the
 // next without leaving the warp: K S^T (A = S), E (A = R), y (A = S and E),
-// S' (A = U).  The warps share only the chunk's tiles, which four further
-// warps prepare one chunk ahead; one barrier a chunk is all the
+// S' (A = U).  The warps share only the chunk's tiles, copied one chunk ahead
+// into the other of two buffers; one barrier a chunk is all the
 // synchronisation there is.
 #pragma once
 
-#include "ssd_delta_core.cuh"
+#include "ssd_delta_prep.cuh"
 
 namespace ssd {
 namespace delta {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kP = 16 * kWarps;  // headdim rows of a CTA, 16 a warp
+
+struct WalkArgs {
+  int64_t L, H, G, P, N, hpg;
+  int slices;          // CTAs over headdim
+  int64_t units;       // (run, head, slice)
+  const char* tokens;  // [chunk][group] TokenTiles
+  const char* heads;   // [chunk][head] HeadTiles
+  const void* v;       // forward: v; reverse: dy
+  const float* s0;     // state a run starts from (reverse: gradient of the final state), or null
+  const Run* runs;     // or null: a run for each row
+  void* out;           // forward: y; state walk: E (fp32); reverse: dv
+  float* out_f;        // reverse: D (fp32)
+  float* check;        // state at every 64th token of a run (state walk, reverse)
+  float* fin;          // final state (forward) or gradient of the initial state (reverse), or null
+  int v_vec, out_vec;  // rows start on 16-byte boundaries
+};
+
+// A chunk's tiles in shared memory, two buffers.
+template <typename T, int NT, bool Q, int MTERMS>
+struct Buffers {
+  using X = TokenTiles<T, NT>;
+  using Hd = HeadTiles<MTERMS>;
+  static constexpr int kTok = Q ? X::kBytes : X::kBytes / 2;  // k, and q where it is used
+  static constexpr int kVP = sizeof(T) == 2 ? kP + 8 : kP + 4;  // row pitch of the V tile
+  static constexpr int kHead = kTok, kV = kHead + Hd::kBytes;
+  static constexpr int kBuf = kV + kC * kVP * (int)sizeof(T);
+  static constexpr int kStage = 2 * kBuf;  // a warp's output tile, fp32 pitch 20
+  static constexpr int kBytes = kStage + kWarps * kC * 20 * 4;
+  static_assert(kBuf % 16 == 0, "16-byte copies");
+};
+
+// Enqueue the copies of one chunk: the group's tiles, the head's, and its rows
+// of V (n of them exist, `cols` columns; the rest become zeros).
+template <typename T, int NT, bool Q, int MTERMS>
+__device__ __forceinline__ void fetch_chunk(const char* tok, const char* head, const T* v, int64_t vstride, int n, int cols,
+                                            bool vec, char* buf) {
+  using B = Buffers<T, NT, Q, MTERMS>;
+  const uint32_t d = sm100::smem_u32(buf);
+#pragma unroll
+  for (int x = 0; x < B::kTok / (16 * kThreads); ++x) {
+    const int o = (x * kThreads + threadIdx.x) * 16;
+    cp_async16(d + o, tok + o, true);
+  }
+  constexpr int kHeadVec = B::Hd::kBytes / 16;
+#pragma unroll
+  for (int x = 0; x < (kHeadVec + kThreads - 1) / kThreads; ++x) {
+    const int i = x * kThreads + threadIdx.x;
+    if (i < kHeadVec) cp_async16(d + B::kHead + i * 16, head + i * 16, true);
+  }
+  constexpr int E = 16 / (int)sizeof(T), PC = kP / E, kStep = kThreads / PC;
+  const int row0 = threadIdx.x / PC, c = (threadIdx.x % PC) * E;
+#pragma unroll
+  for (int x = 0; x < kC / kStep; ++x) {
+    const int row = row0 + x * kStep;
+    const bool ok = row < n && c < cols;
+    const uint32_t o = B::kV + (row * B::kVP + c) * (int)sizeof(T);
+    if (vec) {
+      cp_async16(d + o, ok ? v + row * vstride + c : v, ok);
+    } else {
+      T* dst = reinterpret_cast<T*>(buf + o);
+#pragma unroll 1
+      for (int e = 0; e < E; ++e) dst[e] = ok && c + e < cols ? v[row * vstride + c + e] : from_f<T>(0.f);
+    }
+  }
+  cp_async_commit();
+}
 
 enum WalkMode { kForward = 0, kStates = 1 };
 
@@ -122,9 +191,9 @@ __device__ __forceinline__ float2 to_operand(const float (&x)[4][4], uint32_t (&
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const float s = a & 1 ? s1 : s0;
-      const float u = x[2 * ks + (a >> 1)][2 * (a & 1)] * s, v = x[2 * ks + (a >> 1)][2 * (a & 1) + 1] * s;
-      if constexpr (LO) split2(u, v, hi[ks][a], lo[ks][a]);
-      else hi[ks][a] = pack2(u, v);
+      const float2 u = mul2(x[2 * ks + (a >> 1)][2 * (a & 1)], x[2 * ks + (a >> 1)][2 * (a & 1) + 1], s);
+      if constexpr (LO) split2(u, hi[ks][a], lo[ks][a]);
+      else hi[ks][a] = pack2(u);
     }
   return inv;
 }
@@ -174,7 +243,9 @@ __device__ __forceinline__ void state_max(const float (&S)[NT / 8][4], float& m0
   m0 = quad_max(m0), m1 = quad_max(m1);
 }
 
-// S += Uhi/lo (p x t) times a 32 x NT tile of tokens (k or q; TERMS fp16 terms).
+// S += Uhi/lo (p x t) times a 32 x NT tile of tokens (k or q; TERMS fp16
+// terms).  Four tiles at a time, so that an accumulator is not needed again
+// before its last product is done.
 template <int NT, int TERMS>
 __device__ __forceinline__ void state_add(float (&S)[NT / 8][4], const uint32_t (&hi)[2][4], const uint32_t (&lo)[2][4],
                                           uint32_t tile, int lane) {
@@ -183,80 +254,87 @@ __device__ __forceinline__ void state_add(float (&S)[NT / 8][4], const uint32_t 
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-    for (int np = 0; np < NT / 16; ++np) {
-      uint32_t B[4];
-      ldsm4t(tile + tile_off<NT>(16 * ks + tr, 16 * np + nc), B);
-      mma(S[2 * np], hi[ks], B[0], B[1]);
-      mma(S[2 * np + 1], hi[ks], B[2], B[3]);
-      mma(S[2 * np], lo[ks], B[0], B[1]);
-      mma(S[2 * np + 1], lo[ks], B[2], B[3]);
-      if constexpr (TERMS == 2) {
-        ldsm4t(tile + kTile + tile_off<NT>(16 * ks + tr, 16 * np + nc), B);
-        mma(S[2 * np], hi[ks], B[0], B[1]);
-        mma(S[2 * np + 1], hi[ks], B[2], B[3]);
+    for (int np = 0; np < NT / 16; np += 2) {
+      uint32_t B[2][4];
+#pragma unroll
+      for (int t = 0; t < TERMS; ++t) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) ldsm4t(tile + t * kTile + tile_off<NT>(16 * ks + tr, 16 * (np + x) + nc), B[x]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mma(S[2 * np + x], hi[ks], B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
+        if (t == 0) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mma(S[2 * np + x], lo[ks], B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
+        }
       }
     }
 }
 
-template <typename T, int NT, bool STAGED, int MODE>
-__global__ void __launch_bounds__(kThreads, NT <= 128 && sizeof(T) == 2 ? 2 : 1) k_delta_walk(const WalkArgs a) {
-  using L = Tiles<T, NT, STAGED>;
+// d (p x t) += A (p x NT, hi and lo of one 16-column step) times rows of a
+// 32 x NT tile of tokens; LO: with A's lo term.
+template <int NT, int TERMS, bool LO>
+__device__ __forceinline__ void tokens_mma(float (&d)[4][4], const uint32_t (&hi)[4], const uint32_t (&lo)[4], uint32_t tile,
+                                           int ks, int lane) {
+  constexpr int kTile = kC * NT * 2;
+  const int br = (lane & 7) + (lane >> 4) * 8, bc = ((lane >> 3) & 1) * 8;
+  uint32_t B[2][4];
+#pragma unroll
+  for (int t = 0; t < TERMS; ++t) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) ldsm4(tile + t * kTile + tile_off<NT>(16 * x + br, 16 * ks + bc), B[x]);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) mma(d[x], hi, B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
+    if (LO && t == 0) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mma(d[x], lo, B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
+    }
+  }
+}
+
+// d (p x t) += X (p x s) W^T for a lower triangular 32 x 32 tile W (t x s):
+// X's terms times W's terms, lo times lo left out.
+template <bool XLO, int WTERMS>
+__device__ __forceinline__ void lower_mma(float (&d)[4][4], const uint32_t (&hi)[2][4], const uint32_t (&lo)[2][4],
+                                          uint32_t tile, int lane) {
+  const int br = (lane & 7) + (lane >> 4) * 8, bc = ((lane >> 3) & 1) * 8;
+  uint32_t B[3][4];  // (t, s) blocks of 16: (0, 0), (1, 0), (1, 1)
+#pragma unroll
+  for (int w = 0; w < WTERMS; ++w) {
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+      ldsm4(tile + w * kSq + tile_off<32>(16 * (x > 0) + br, 16 * (x == 2) + bc), B[x]);
+#pragma unroll
+    for (int x = 0; x < 6; ++x)
+      mma(d[x < 4 ? x : x - 2], hi[x >> 2], B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
+    if (XLO && w == 0) {
+#pragma unroll
+      for (int x = 0; x < 6; ++x)
+        mma(d[x < 4 ? x : x - 2], lo[x >> 2], B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
+    }
+  }
+}
+
+template <typename T, int NT, int MODE>
+__global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(const WalkArgs a) {
   constexpr bool kY = MODE == kForward;
-  extern __shared__ __align__(1024) char sm[];
-  const uint32_t smu = sm100::smem_u32(sm);
+  constexpr int kMTerms = !kY ? 0 : sizeof(T) == 4 ? 2 : 1;
+  using B = Buffers<T, NT, kY, kMTerms>;
+  using X = TokenTiles<T, NT>;
+  using Hd = HeadTiles<kMTerms>;
+  constexpr int kTerms = X::kTerms;
+  extern __shared__ __align__(128) char sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slice = blockIdx.x % a.slices;
   const int64_t rh = blockIdx.x / a.slices, h = rh % a.H, ri = rh / a.H;
-  Run run;
-  if (a.runs) {
-    run = a.runs[ri];
-  } else {
-    run.tok = ri * a.L, run.len = (int)a.L, run.fin = run.h0 = (int)ri;
-    run.slot = ri * ((a.L + kCheck - 1) / kCheck);
-  }
+  const Run run = a.runs ? a.runs[ri] : row_run(ri, a.L);
   const int nc = (run.len + kC - 1) / kC;
-  const int p_cta = slice * kP;
-  if (warp >= kStateWarps) {  // ---- the warps that prepare the tiles
-    const int pw = warp - kStateWarps, pt = threadIdx.x - kStateThreads;
-    const int64_t grp = h / a.hpg;
-    PrepSrc<T> s;
-    s.k = static_cast<const T*>(a.k) + (run.tok * a.G + grp) * a.N;
-    s.q = static_cast<const T*>(a.q) + (run.tok * a.G + grp) * a.N;
-    s.v = static_cast<const T*>(a.v) + (run.tok * a.H + h) * a.P + p_cta;
-    s.g = a.g + run.tok * a.H + h;
-    s.beta = a.beta + run.tok * a.H + h;
-    s.len = run.len;
-    s.P = (int)(a.P - p_cta < kP ? a.P - p_cta : kP);
-    const auto gate = [&](int j, const float* src) {
-      const int t = j * kC + lane;
-      return pw == 0 && t < run.len ? src[t * a.H] : 0.f;
-    };
-    float gv = gate(0, s.g), bv = gate(0, s.beta);
-    if (nc > 0) {
-      prep_issue<T, NT, STAGED>(a, s, 0, sm, smu, pt);
-      prep_issue<T, NT, STAGED>(a, s, 1, sm, smu, pt);
-      cp_async_wait<1>();
-      prep_sync();
-      prep_chunk<T, NT, STAGED, false, kY>(a, s, 0, gv, bv, sm, smu, pw, lane);
-    }
-    gv = gate(1, s.g), bv = gate(1, s.beta);
-    __syncthreads();
-    for (int j = 0; j < nc; ++j) {
-      if (j + 1 < nc) {
-        const float g1 = gate(j + 2, s.g), b1 = gate(j + 2, s.beta);
-        prep_issue<T, NT, STAGED>(a, s, j + 2, sm, smu, pt);
-        cp_async_wait<1>();
-        prep_sync();
-        prep_chunk<T, NT, STAGED, false, kY>(a, s, j + 1, gv, bv, sm, smu, pw, lane);
-        gv = g1, bv = b1;
-      }
-      __syncthreads();
-    }
-    return;
-  }
-  // ---- the warps that carry the state: rows p0..p0+15
-  const int p0 = p_cta + 16 * warp;
+  const int p_cta = slice * kP, p0 = p_cta + 16 * warp;
+  const int cols = (int)(a.P - p_cta < kP ? a.P - p_cta : kP);
   const int rows = a.P - p0 < 16 ? (int)(a.P - p0) : 16;  // may be negative: nothing is read or written
+  const int64_t vstride = a.H * a.P, tstride = a.G * X::kBytes, hstride = a.H * Hd::kBytes;
+  const char* tok = a.tokens + (run.chunk * a.G + h / a.hpg) * X::kBytes;
+  const char* head = a.heads + (run.chunk * a.H + h) * Hd::kBytes;
+  const T* v = static_cast<const T*>(a.v) + (run.tok * a.H + h) * a.P + p_cta;
   float S[NT / 8][4];
   float sig0 = 1.f, sig1 = 1.f;  // the state's rows are S times these
   if (a.s0 && run.h0 >= 0) {
@@ -267,18 +345,23 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 && sizeof(T) == 2 ? 2 : 1)
 #pragma unroll
       for (int e = 0; e < 4; ++e) S[i][e] = 0.f;
   }
-  char* stage = sm + L::kStage + warp * (kC * 20 * 4);
-  const int br = (lane & 7) + (lane >> 4) * 8, bc = ((lane >> 3) & 1) * 8;
-  __syncthreads();
+  char* stage = sm + B::kStage + warp * (kC * 20 * 4);
+  sm100::griddep_wait();  // the tiles
+  const auto fetch = [&](int j) {
+    const int n = run.len - j * kC;
+    fetch_chunk<T, NT, kY, kMTerms>(tok + j * tstride, head + j * hstride, v + (int64_t)j * kC * vstride, vstride, n, cols,
+                                    a.v_vec, sm + (j & 1) * B::kBuf);
+  };
+  if (nc > 0) fetch(0);
   for (int j = 0; j < nc; ++j) {
-    if (rows <= 0) {  // no such rows: only keep step
-      __syncthreads();
-      continue;
-    }
-    const int buf = j & 1;
-    const Factors& f = reinterpret_cast<const Factors*>(sm + L::kFac)[buf];
-    const uint32_t kt = smu + L::kK + buf * L::kTerms * L::kTile, qt = smu + L::kQ + buf * L::kTerms * L::kTile;
-    const uint32_t tt = smu + L::kT + buf * 2 * L::kSq, mt = smu + L::kM + buf * 2 * L::kSq;
+    cp_async_wait<0>();
+    __syncthreads();  // chunk j is there, and every warp is done with the other buffer
+    if (j + 1 < nc) fetch(j + 1);
+    if (rows <= 0) continue;  // no such rows: only keep step
+    char* const buf = sm + (j & 1) * B::kBuf;
+    const Factors& f = *reinterpret_cast<const Factors*>(buf + B::kHead + Hd::kF);
+    const uint32_t kt = sm100::smem_u32(buf), qt = kt + kTerms * X::kTile;
+    const uint32_t tt = kt + B::kHead, mt = tt + Hd::kM;
     if constexpr (MODE == kStates) {
       if ((j & 1) == 0)
         store_state<NT>(S, sig0, sig1, a.check + (((run.slot + (j >> 1)) * a.H + h) * a.P + p0) * a.N, a.N, rows, lane);
@@ -294,36 +377,10 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 && sizeof(T) == 2 ? 2 : 1)
     for (int ks = 0; ks < NT / 16; ++ks) {
       uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float sc = x & 1 ? sc1 : sc0;
-        split2(S[2 * ks + (x >> 1)][2 * (x & 1)] * sc, S[2 * ks + (x >> 1)][2 * (x & 1) + 1] * sc, hi[x], lo[x]);
-      }
-#pragma unroll
-      for (int np = 0; np < 2; ++np) {
-        uint32_t B[4];
-        ldsm4(kt + tile_off<NT>(16 * np + br, 16 * ks + bc), B);
-        mma(acc[2 * np], hi, B[0], B[1]);
-        mma(acc[2 * np + 1], hi, B[2], B[3]);
-        mma(acc[2 * np], lo, B[0], B[1]);
-        mma(acc[2 * np + 1], lo, B[2], B[3]);
-        if constexpr (L::kTerms == 2) {
-          ldsm4(kt + L::kTile + tile_off<NT>(16 * np + br, 16 * ks + bc), B);
-          mma(acc[2 * np], hi, B[0], B[1]);
-          mma(acc[2 * np + 1], hi, B[2], B[3]);
-        }
-        if constexpr (kY) {
-          ldsm4(qt + tile_off<NT>(16 * np + br, 16 * ks + bc), B);
-          mma(yq[2 * np], hi, B[0], B[1]);
-          mma(yq[2 * np + 1], hi, B[2], B[3]);
-          if constexpr (L::kTerms == 2) {
-            mma(yq[2 * np], lo, B[0], B[1]);
-            mma(yq[2 * np + 1], lo, B[2], B[3]);
-            ldsm4(qt + L::kTile + tile_off<NT>(16 * np + br, 16 * ks + bc), B);
-            mma(yq[2 * np], hi, B[0], B[1]);
-            mma(yq[2 * np + 1], hi, B[2], B[3]);
-          }
-        }
-      }
+      for (int x = 0; x < 4; ++x)
+        split2(mul2(S[2 * ks + (x >> 1)][2 * (x & 1)], S[2 * ks + (x >> 1)][2 * (x & 1) + 1], x & 1 ? sc1 : sc0), hi[x], lo[x]);
+      tokens_mma<NT, kTerms, true>(acc, hi, lo, kt, ks, lane);
+      if constexpr (kY) tokens_mma<NT, kTerms, kTerms == 2>(yq, hi, lo, qt, ks, lane);
     }
     const int tc = 2 * (lane & 3);
     uint32_t hi[2][4], lo[2][4];
@@ -331,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 && sizeof(T) == 2 ? 2 : 1)
     float2 iv;
     {  // R = V - exp(cs) K S^T
       float v[4][4];
-      load_v<T, L::kVP>(v, sm + L::kV + (j % 3) * L::kVTile, 16 * warp, lane);
+      load_v<T, B::kVP>(v, buf + B::kV, 16 * warp, lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 kc = *reinterpret_cast<const float2*>(f.kc + 8 * i + tc);
@@ -342,21 +399,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 && sizeof(T) == 2 ? 2 : 1)
       }
       iv = to_operand<true>(v, hi, lo);
     }
-    zero(e);  // E = R (I + A)^-T, its lower triangle
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int np = ks; np < 2; ++np) {
-        uint32_t B[4];
-        ldsm4(tt + tile_off<32>(16 * np + br, 16 * ks + bc), B);
-        mma(e[2 * np], hi[ks], B[0], B[1]);
-        mma(e[2 * np + 1], hi[ks], B[2], B[3]);
-        mma(e[2 * np], lo[ks], B[0], B[1]);
-        mma(e[2 * np + 1], lo[ks], B[2], B[3]);
-        ldsm4(tt + L::kSq + tile_off<32>(16 * np + br, 16 * ks + bc), B);
-        mma(e[2 * np], hi[ks], B[0], B[1]);
-        mma(e[2 * np + 1], hi[ks], B[2], B[3]);
-      }
+    zero(e);  // E = R (I + A)^-T
+    lower_mma<true, 2>(e, hi, lo, tt, lane);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 tau = *reinterpret_cast<const float2*>(f.tau + 8 * i + tc);
@@ -365,24 +409,9 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 && sizeof(T) == 2 ? 2 : 1)
     const int n = run.len - j * kC < kC ? run.len - j * kC : kC;
     const int64_t row0 = ((run.tok + (int64_t)j * kC) * a.H + h) * a.P + p0;
     if constexpr (kY) {
-      iv = to_operand<L::kTerms == 2>(e, hi, lo);
+      iv = to_operand<kTerms == 2>(e, hi, lo);
       zero(acc);
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-        for (int np = ks; np < 2; ++np) {
-          uint32_t B[4];
-          ldsm4(mt + tile_off<32>(16 * np + br, 16 * ks + bc), B);
-          mma(acc[2 * np], hi[ks], B[0], B[1]);
-          mma(acc[2 * np + 1], hi[ks], B[2], B[3]);
-          if constexpr (L::kTerms == 2) {
-            mma(acc[2 * np], lo[ks], B[0], B[1]);
-            mma(acc[2 * np + 1], lo[ks], B[2], B[3]);
-            ldsm4(mt + L::kSq + tile_off<32>(16 * np + br, 16 * ks + bc), B);
-            mma(acc[2 * np], hi[ks], B[0], B[1]);
-            mma(acc[2 * np + 1], hi[ks], B[2], B[3]);
-          }
-        }
+      lower_mma<kTerms == 2, kMTerms>(acc, hi, lo, mt, lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 qc = *reinterpret_cast<const float2*>(f.qc + 8 * i + tc);
@@ -413,44 +442,47 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 && sizeof(T) == 2 ? 2 : 1)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const float s = x & 1 ? su1 : su0;
-        split2(e[2 * ks + (x >> 1)][2 * (x & 1)] * s, e[2 * ks + (x >> 1)][2 * (x & 1) + 1] * s, hi[ks][x], lo[ks][x]);
+        split2(mul2(e[2 * ks + (x >> 1)][2 * (x & 1)], e[2 * ks + (x >> 1)][2 * (x & 1) + 1], s), hi[ks][x], lo[ks][x]);
       }
     const float w0 = f.whole * sig0 * su0, w1 = f.whole * sig1 * su1;
 #pragma unroll
-    for (int i = 0; i < NT / 8; ++i) S[i][0] *= w0, S[i][1] *= w0, S[i][2] *= w1, S[i][3] *= w1;
+    for (int i = 0; i < NT / 8; ++i) {
+      const float2 x = mul2(S[i][0], S[i][1], w0), y = mul2(S[i][2], S[i][3], w1);
+      S[i][0] = x.x, S[i][1] = x.y, S[i][2] = y.x, S[i][3] = y.y;
+    }
     sig0 = n0, sig1 = n1;
-    state_add<NT, L::kTerms>(S, hi, lo, kt, lane);
-    __syncthreads();
+    state_add<NT, kTerms>(S, hi, lo, kt, lane);
   }
   if (a.fin && run.fin >= 0)
     store_state<NT>(S, sig0, sig1, a.fin + (((int64_t)run.fin * a.H + h) * a.P + p0) * a.N, a.N, rows, lane);
 }
 
-template <typename T, int NT, bool STAGED, int MODE>
-cudaError_t launch_walk(const WalkArgs& a, cudaStream_t stream) {
-  constexpr int smem = Tiles<T, NT, STAGED>::kBytes;
-  static_assert(smem <= 227 * 1024, "shared memory");
-  const cudaError_t e =
-      cudaFuncSetAttribute(k_delta_walk<T, NT, STAGED, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// Launch a walk; its CTAs may start while the tiles' kernel ends.
+template <typename K, typename A>
+cudaError_t launch_after(K kern, unsigned grid, int smem, const A& args, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  k_delta_walk<T, NT, STAGED, MODE><<<(unsigned)a.n_units, kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid), c.blockDim = dim3(kThreads), c.dynamicSmemBytes = smem, c.stream = stream;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at, c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, args);
+}
+
+template <typename T, int NT, int MODE>
+cudaError_t launch_walk_nt(const WalkArgs& a, cudaStream_t stream) {
+  constexpr int smem = Buffers<T, NT, MODE == kForward, MODE != kForward ? 0 : sizeof(T) == 4 ? 2 : 1>::kBytes;
+  static_assert(smem <= 227 * 1024, "shared memory");
+  return launch_after(k_delta_walk<T, NT, MODE>, (unsigned)a.units, smem, a, stream);
 }
 
 template <typename T, int MODE>
-cudaError_t launch_walk_any(const WalkArgs& a, cudaStream_t stream) {
-  // 16-byte copies need rows on 16-byte boundaries; fp32 tiles are read where they lie
-  const bool staged = sizeof(T) == 2 && a.qk_vec;
-  if constexpr (sizeof(T) == 2) {
-    if (staged) {
-      if (a.N <= 64) return launch_walk<T, 64, true, MODE>(a, stream);
-      if (a.N <= 128) return launch_walk<T, 128, true, MODE>(a, stream);
-      return launch_walk<T, 256, true, MODE>(a, stream);
-    }
-  }
-  if (a.N <= 64) return launch_walk<T, 64, false, MODE>(a, stream);
-  if (a.N <= 128) return launch_walk<T, 128, false, MODE>(a, stream);
-  return launch_walk<T, 256, false, MODE>(a, stream);
+cudaError_t launch_walk(const WalkArgs& a, cudaStream_t stream) {
+  if (a.N <= 64) return launch_walk_nt<T, 64, MODE>(a, stream);
+  if (a.N <= 128) return launch_walk_nt<T, 128, MODE>(a, stream);
+  return launch_walk_nt<T, 256, MODE>(a, stream);
 }
 
 }  // namespace delta

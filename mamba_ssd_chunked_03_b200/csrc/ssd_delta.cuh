@@ -42,6 +42,15 @@ struct Chunk {
   int32_t tok, n;
 };
 
+// A checkpoint's place: the (up to) 64 tokens it covers, their first chunk; for
+// the last ones of a run the index of its final state, and for the first ones
+// the row whose initial state it starts from (-1: none; kInside: not the last,
+// or first, ones).
+constexpr int kInside = -2;
+struct Slot {
+  int32_t tok, n, chunk, fin, h0;
+};
+
 // ---------------------------------------------------------------- elements
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -157,6 +166,7 @@ __device__ __forceinline__ Run row_run(int64_t ri, int64_t L) {
 struct RunList {
   Run* runs;
   Chunk* chunks;
+  Slot* slots;
   int32_t* first;
   int32_t* present;
 };

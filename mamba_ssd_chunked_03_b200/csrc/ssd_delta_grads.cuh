@@ -1,0 +1,589 @@
+// The gradients of the gated delta rule that need no further walk.  For 64
+// tokens of a head, with S the state that enters them, dS the gradient of the
+// state that leaves them, e_t and d_t from the walks (u = beta e, dv = beta d),
+// cs the cumulative sum of g over the 64, Gam_ts = exp(cs_t - cs_s):
+//
+//   P_ts = scale Gam_ts beta_s dy_t.e_s (s <= t),  Z_ts = -Gam_ts beta_t beta_s d_t.e_s (s < t)
+//   dq = P K + scale exp(cs) dY S
+//   dk = P^T Q + (Z + Z^T) K - beta exp(cs) D S + exp(cs_C - cs) beta E dS
+//   dbeta_t = d_t.e_t
+//   dg_t = sum_{s >= t} (dq_s.q_s - dv_s.v_s) + <dS, S_C>     (this head's dq; S_C the state that leaves)
+//
+// dg by the last line takes each token's pi_t = <G_t, S_t> from the next one's
+// (pi_{t-1} = dg_t + dy_{t-1}.y_{t-1}, dg_t = pi_t - dv_t.v_t, and dy.y = dq.q).
+// <dS, S> is known at both ends of the 64 tokens (dg_0 is that of the tokens
+// before), so the sums run from the nearer end, over 32 tokens at most, and
+// rounding does not pile up along the sequence.  dq is therefore held to fp32
+// accuracy (split operands), dk only to its type's.
+//
+// One CTA takes 64 tokens of a group, a slice of the columns n, and some of the
+// group's heads, whose dq and dk it adds in registers in a fixed order; eight
+// warps: four times 16 rows, two halves of the columns.
+#pragma once
+
+#include "ssd_delta_prep.cuh"
+
+namespace ssd {
+namespace delta {
+
+constexpr int kGradThreads = 256;
+constexpr int kPS = 64;  // headdim columns staged at once
+
+struct GradArgs {
+  int64_t L, H, G, P, N, hpg;
+  int per_row;        // checkpoints of a row, without a list
+  int splits, heads;  // CTAs that share a group's heads, heads of each
+  int nslices;        // slices of the columns n
+  int pg;
+  float scale;
+  const char* tokens;  // TokenTiles of both 32-token chunks
+  const char* head;    // HeadTiles<2> of the reverse walk: factors
+  const void* v;
+  const void* dy;
+  const float* e;
+  const float* d;
+  const float* s;       // [slot][head][P][N] states that enter
+  const float* ds;      // gradients of the states that leave
+  const float* s_fin;   // [run][head][P][N] last states, or null (no gradient comes in there)
+  const float* g;
+  const float* beta;
+  const float *max_y, *max_e, *max_d, *max_s, *max_ds;
+  const Slot* slots;    // packed, or null
+  void* dq;
+  void* dk;
+  float* part;          // [split][2][tokens][G][N], with several splits
+  int64_t part_size;    // tokens G N
+  float* qdq;           // [nslice][tokens][H]
+  int64_t part_stride;  // tokens H
+  float* dvv;           // [tokens][H]
+  float* pi;            // [nslice][slot][H]
+  float* dbeta;
+  int64_t slots_n;
+  int vec;              // rows of v and dy can be read by fours
+  bool initial;         // there are initial states
+  int pair;             // dq and dk can be written by twos
+};
+
+// Sizes of the shared tiles of k_delta_grads, in bytes.
+template <typename T, int NT>
+struct GradTiles {
+  static constexpr int kTerms = sizeof(T) == 2 ? 1 : 2;
+  static constexpr int kNS = sizeof(T) == 4 || NT == 64 ? 64 : 128;  // columns n of a CTA
+  static constexpr int kTok = 64 * kNS * 2, kSmall = 64 * 64 * 2;
+  static constexpr int kK = 0, kQ = kK + kTerms * kTok;
+  static constexpr int kS = kQ + kTerms * kTok;        // hi, lo
+  static constexpr int kDS = kS + 2 * kTok;            // terms
+  static constexpr int kE = kDS + kTerms * kTok;       // hi, lo
+  static constexpr int kD = kE + 2 * kSmall;           // terms
+  static constexpr int kY = kD + kTerms * kSmall;      // terms
+  static constexpr int kW1 = kY + kTerms * kSmall;     // P with k's scales, hi, lo
+  static constexpr int kW2 = kW1 + 2 * kSmall;         // P with q's scales, terms
+  static constexpr int kZa = kW2 + kTerms * kSmall;    // Z with k's scales by row
+  static constexpr int kZb = kZa + kTerms * kSmall;    // Z with k's scales by column
+  static constexpr int kBytes = kZb + kTerms * kSmall;
+};
+
+// A operand: rows row0.., columns col0.. of a row-major tile W wide; or, TRANS,
+// the transpose of a tile stored by rows of k.
+template <int W, bool TRANS>
+__device__ __forceinline__ void a_frag(uint32_t tile, int row0, int col0, int lane, uint32_t (&r)[4]) {
+  if constexpr (!TRANS) ldsm4(tile + tile_off<W>(row0 + (lane & 15), col0 + (lane >> 4) * 8), r);
+  else ldsm4t(tile + tile_off<W>(col0 + ((lane >> 4) & 1) * 8 + (lane & 7), row0 + ((lane >> 3) & 1) * 8), r);
+}
+
+// acc (16 x 8 TN) += A (rows m0.., k steps k0..k1) B, B stored by rows of k
+// (columns n0..): TA, TB terms, lo times lo left out.  ATRANS: A is stored by
+// rows of k too.
+template <int TN, int AW, bool ATRANS, int TA, int BW, int TB>
+__device__ __forceinline__ void product(float (&acc)[TN][4], uint32_t a, int as, int m0, uint32_t b, int bs, int n0, int k0,
+                                        int k1, int lane) {
+  const int tr = (lane & 7) + ((lane >> 3) & 1) * 8, nc = (lane >> 4) * 8;
+#pragma unroll 1
+  for (int k = k0; k < k1; ++k) {
+    uint32_t A[TA][4];
+#pragma unroll
+    for (int t = 0; t < TA; ++t) a_frag<AW, ATRANS>(a + t * as, m0, 16 * k, lane, A[t]);
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+#pragma unroll
+      for (int np = 0; np < TN / 2; np += 2) {
+        uint32_t B[2][4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) ldsm4t(b + t * bs + tile_off<BW>(16 * k + tr, n0 + 16 * (np + x) + nc), B[x]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mma(acc[2 * np + x], A[0], B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
+        if (TA == 2 && t == 0) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) mma(acc[2 * np + x], A[TA - 1], B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
+        }
+      }
+  }
+}
+
+template <int TN>
+__device__ __forceinline__ void clear(float (&x)[TN][4]) {
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
+}
+// to += x times a factor for each of the two rows
+template <int TN>
+__device__ __forceinline__ void add_rows(float (&to)[TN][4], const float (&x)[TN][4], float f0, float f1) {
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    to[i][0] = fmaf(x[i][0], f0, to[i][0]), to[i][1] = fmaf(x[i][1], f0, to[i][1]);
+    to[i][2] = fmaf(x[i][2], f1, to[i][2]), to[i][3] = fmaf(x[i][3], f1, to[i][3]);
+  }
+}
+
+// four scaled values as fp16 terms at byte offset o of a tile
+template <int TERMS>
+__device__ __forceinline__ void put4(char* tile, int term_bytes, uint32_t o, const float (&x)[4], float sc) {
+  uint32_t h0, l0, h1, l1;
+  split2(mul2(x[0], x[1], sc), h0, l0);
+  split2(mul2(x[2], x[3], sc), h1, l1);
+  *reinterpret_cast<uint2*>(tile + o) = make_uint2(h0, h1);
+  if constexpr (TERMS == 2) *reinterpret_cast<uint2*>(tile + term_bytes + o) = make_uint2(l0, l1);
+}
+
+// four elements of a row, zeros where there are none
+template <typename T>
+__device__ __forceinline__ void get4(const T* p, int left, bool vec, float (&x)[4]) {
+  if (left >= 4 && vec) {
+    if constexpr (sizeof(T) == 2) {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+      const float2 a = bf16x2(u.x), b = bf16x2(u.y);
+      x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+    } else {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(p));
+      x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = e < left ? to_f(p[e]) : 0.f;
+  }
+}
+
+// The slot of a call without a list.
+__device__ __forceinline__ Slot row_slot(const GradArgs& a, int64_t slot) {
+  const int64_t row = slot / a.per_row, i = slot % a.per_row;
+  Slot s;
+  s.tok = (int)(row * a.L + i * kCheck), s.n = a.L - i * kCheck < kCheck ? (int)(a.L - i * kCheck) : kCheck;
+  s.chunk = (int)(row * ((a.L + kC - 1) / kC) + 2 * i);
+  s.fin = i + 1 < a.per_row ? kInside : (int)row, s.h0 = i > 0 ? kInside : (int)row;
+  return s;
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs a) {
+  using G = GradTiles<T, NT>;
+  using X = TokenTiles<T, NT>;
+  constexpr int NS = G::kNS, TM = G::kTerms, TN = NS / 16;  // accumulator tiles of a warp: half the columns
+  extern __shared__ __align__(128) char sm[];
+  __shared__ double cs[kCheck];
+  __shared__ __align__(16) float into[kCheck], outof[kCheck], inv[kCheck], bet[kCheck];
+  __shared__ float sums[3][kCheck];     // d.e, dv.v, and q.dq of the second half of the columns
+  __shared__ float wmax[3][8], wpi[8];
+  __shared__ int plain_s;
+  const uint32_t smu = sm100::smem_u32(sm);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mt = warp & 3, half = warp >> 2;
+  int64_t u = blockIdx.x;
+  const int split = (int)(u % a.splits);
+  u /= a.splits;
+  const int ns = (int)(u % a.nslices);
+  u /= a.nslices;
+  const int64_t grp = u % a.G, slot = u / a.G;
+  const Slot sl = a.slots ? a.slots[slot] : row_slot(a, slot);
+  if (sl.n == 0) return;
+  const int nch = sl.n > kC ? 2 : 1, n0 = ns * NS;
+  // the group's k and q: this slice of both chunks' images
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+    for (int i = threadIdx.x; i < TM * 64 * (NS / 8); i += kGradThreads) {
+      const int t = i / (64 * (NS / 8)), r = i / (NS / 8) % 64, c = i % (NS / 8);
+      const char* src = a.tokens + ((int64_t)(sl.chunk + (r >> 5)) * a.G + grp) * X::kBytes + (w * TM + t) * X::kTile +
+                        (r & 31) * (NT * 2) + n0 * 2 + c * 16;
+      const uint32_t dst = (w ? G::kQ : G::kK) + t * G::kTok + r * (NS * 2) + c * 16;
+      *reinterpret_cast<uint4*>(sm + dst) =
+          r < kC * nch ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+    }
+  float dq[TN][4], dk[TN][4];
+  clear(dq);
+  clear(dk);
+  const int r0 = 16 * mt + (lane >> 2);  // this thread's rows: r0, r0 + 8
+  const int64_t h1 = grp * a.hpg + ((int64_t)(split + 1) * a.heads < a.hpg ? (int64_t)(split + 1) * a.heads : a.hpg);
+  for (int64_t h = grp * a.hpg + (int64_t)split * a.heads; h < h1; ++h) {
+    __syncthreads();  // the previous head's tiles are read
+    if (warp == 0) {  // the 64 tokens' decays
+      double c2[2];
+      float b2[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        const int64_t o = ((int64_t)sl.tok + t) * a.H + h;
+        c2[i] = decay_log2(t < sl.n ? a.g[o] : 0.f);
+        b2[i] = t < sl.n ? a.beta[o] : 0.f;
+      }
+      double sum = c2[0] + c2[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+      }
+      const double end = __shfl_sync(0xffffffffu, sum, 31);
+      const double v[2] = {sum - c2[1], sum};
+      const bool plain = __all_sync(0xffffffffu, fabs(v[0]) <= 100.0 && fabs(v[1]) <= 100.0);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        cs[t] = v[i], into[t] = pow2_of(v[i]), outof[t] = pow2_of(end - v[i]), inv[t] = plain ? pow2_of(-v[i]) : 0.f;
+        bet[t] = b2[i];
+      }
+      if (lane == 0) plain_s = plain;
+    }
+    if (threadIdx.x < kCheck) sums[0][threadIdx.x] = sums[1][threadIdx.x] = 0.f;
+    const Factors* f = reinterpret_cast<const Factors*>(a.head + ((int64_t)sl.chunk * a.H + h) * HeadTiles<2>::kBytes +
+                                                        HeadTiles<2>::kF);
+    const Factors* f1 = reinterpret_cast<const Factors*>(reinterpret_cast<const char*>(f) +
+                                                         (nch == 2 ? a.H * HeadTiles<2>::kBytes : 0));
+    const float ik[2] = {f->ik, f1->ik}, iq[2] = {f->iq, f1->iq};
+    float P[2][2][4], Z[2][2][4], dqh[TN][4];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) clear(P[b]), clear(Z[b]);
+    clear(dqh);
+    float pi = 0.f;
+    for (int p0 = 0; p0 < a.P; p0 += kPS) {
+      // the scales: largest magnitudes the walks left, by 16 rows of the state
+      float my = 0.f, me = 0.f, md = 0.f, ms = 0.f, mds = 0.f;
+      for (int i = p0 / 16; i < a.pg && i < p0 / 16 + kPS / 16; ++i) {
+        for (int c = 0; c < nch; ++c) {
+          const int64_t o = ((int64_t)(sl.chunk + c) * a.H + h) * a.pg + i;
+          my = fmaxf(my, a.max_y[o]), me = fmaxf(me, a.max_e[o]), md = fmaxf(md, a.max_d[o]);
+        }
+        const int64_t o = (slot * a.H + h) * a.pg + i;
+        ms = fmaxf(ms, a.max_s[o]), mds = fmaxf(mds, a.max_ds[o]);
+      }
+      float iy, ie, id, is, ids;
+      const float sy = pow2_scale(my, iy), se = pow2_scale(me, ie), sd = pow2_scale(md, id), ss = pow2_scale(ms, is),
+                  sds = pow2_scale(mds, ids);
+      __syncthreads();  // the factors are there; the previous slice's tiles are read
+      const bool v4 = a.P % 4 == 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int t = (threadIdx.x >> 4) + 16 * x, p = (threadIdx.x & 15) * 4;
+        const int left = t < sl.n ? (int)(a.P - p0 - p) : 0;
+        const int64_t o = (((int64_t)sl.tok + t) * a.H + h) * a.P + p0 + p;
+        float e4[4], d4[4], v4v[4], y4[4];
+        get4(a.e + o, left, v4, e4);
+        get4(a.d + o, left, v4, d4);
+        get4(static_cast<const T*>(a.dy) + o, left, a.vec, y4);
+        get4(static_cast<const T*>(a.v) + o, left, a.vec, v4v);
+        float de = 0.f, dv = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) de = fmaf(d4[i], e4[i], de), dv = fmaf(d4[i], v4v[i], dv);
+#pragma unroll
+        for (int i = 8; i > 0; i >>= 1) {
+          de += __shfl_xor_sync(0xffffffffu, de, i);
+          dv += __shfl_xor_sync(0xffffffffu, dv, i);
+        }
+        if ((lane & 15) == 0) sums[0][t] += de, sums[1][t] += dv;  // one thread of its own for each t
+        const uint32_t to = tile_off<64>(t, p);
+        put4<2>(sm + G::kE, G::kSmall, to, e4, se);
+        put4<TM>(sm + G::kD, G::kSmall, to, d4, sd);
+        put4<TM>(sm + G::kY, G::kSmall, to, y4, sy);
+      }
+      const bool n4 = a.N % 4 == 0;
+      const float* sc = sl.fin == kInside ? a.s + (slot + 1) * a.H * a.P * a.N
+                        : a.s_fin && sl.fin >= 0 ? a.s_fin + (int64_t)sl.fin * a.H * a.P * a.N : nullptr;
+      for (int i = threadIdx.x; i < kPS * (NS / 4); i += kGradThreads) {
+        const int p = i / (NS / 4), n = (i % (NS / 4)) * 4;
+        const int left = p0 + p < a.P ? (int)(a.N - n0 - n) : 0;
+        const int64_t o = (h * a.P + p0 + p) * a.N + n0 + n, ol = slot * a.H * a.P * a.N + o;
+        float x[4], y[4], z[4];
+        get4(a.s + ol, left, n4, x);
+        get4(a.ds + ol, left, n4, y);
+        if (sc) {
+          get4(sc + o, left, n4, z);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pi = fmaf(y[e], z[e], pi);
+        }
+        const uint32_t to = tile_off<NS>(p, n);
+        put4<2>(sm + G::kS, G::kTok, to, x, ss);
+        put4<TM>(sm + G::kDS, G::kTok, to, y, sds);
+      }
+      __syncthreads();
+      // dY E^T and D E^T, blocks of 16 tokens on and below the diagonal
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int sb = 2 * half + b;
+        if (sb > mt) continue;
+        float x[2][4], z[2][4];
+        clear(x);
+        clear(z);
+        const int br = (lane & 7) + (lane >> 4) * 8, bc = ((lane >> 3) & 1) * 8;
+#pragma unroll
+        for (int k = 0; k < kPS / 16; ++k) {
+          uint32_t Y[TM][4], D[TM][4], E[2][4];
+#pragma unroll
+          for (int t = 0; t < TM; ++t) {
+            a_frag<64, false>(smu + G::kY + t * G::kSmall, 16 * mt, 16 * k, lane, Y[t]);
+            a_frag<64, false>(smu + G::kD + t * G::kSmall, 16 * mt, 16 * k, lane, D[t]);
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) ldsm4(smu + G::kE + t * G::kSmall + tile_off<64>(16 * sb + br, 16 * k + bc), E[t]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mma(x[i], Y[0], E[0][2 * i], E[0][2 * i + 1]);
+            mma(z[i], D[0], E[0][2 * i], E[0][2 * i + 1]);
+            mma(x[i], Y[0], E[1][2 * i], E[1][2 * i + 1]);
+            if constexpr (TM == 2) {
+              mma(x[i], Y[1], E[0][2 * i], E[0][2 * i + 1]);
+              mma(z[i], D[0], E[1][2 * i], E[1][2 * i + 1]);
+              mma(z[i], D[1], E[0][2 * i], E[0][2 * i + 1]);
+            }
+          }
+        }
+        add_rows(P[b], x, iy * ie, iy * ie);
+        add_rows(Z[b], z, id * ie, id * ie);
+      }
+      float tmp[TN][4];
+      const int nb = half * (NS / 2);
+      clear(tmp);
+      product<TN, 64, false, TM, NS, 2>(tmp, smu + G::kY, G::kSmall, 16 * mt, smu + G::kS, G::kTok, nb, 0, kPS / 16, lane);
+      add_rows(dqh, tmp, a.scale * into[r0] * (iy * is), a.scale * into[r0 + 8] * (iy * is));
+      clear(tmp);
+      product<TN, 64, false, TM, NS, TM>(tmp, smu + G::kD, G::kSmall, 16 * mt, smu + G::kS, G::kTok, nb, 0, kPS / 16, lane);
+      add_rows(dk, tmp, -bet[r0] * into[r0] * (id * is), -bet[r0 + 8] * into[r0 + 8] * (id * is));
+      clear(tmp);
+      product<TN, 64, false, TM, NS, TM>(tmp, smu + G::kE, G::kSmall, 16 * mt, smu + G::kDS, G::kTok, nb, 0, kPS / 16, lane);
+      add_rows(dk, tmp, bet[r0] * outof[r0] * (ie * ids), bet[r0 + 8] * outof[r0 + 8] * (ie * ids));
+    }
+    // P and Z with their decays; the scales of the chunks' k and q go with the
+    // token that is summed over
+    float m1 = 0.f, m2 = 0.f, m3 = 0.f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int sb = 2 * half + b;
+      if (sb > mt) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = r0 + 8 * (e >> 1), s = 16 * sb + 8 * i + 2 * (lane & 3) + (e & 1);
+          float w = 0.f;
+          if (s <= t) w = (plain_s ? into[t] * inv[s] : pow2_of(cs[t] - cs[s])) * bet[s];
+          P[b][i][e] *= a.scale * w;
+          Z[b][i][e] *= s < t ? -bet[t] * w : 0.f;
+          m1 = fmaxf(m1, fabsf(P[b][i][e]) * ik[s >> 5]);
+          m2 = fmaxf(m2, fabsf(P[b][i][e]) * iq[t >> 5]);
+          m3 = fmaxf(m3, fabsf(Z[b][i][e]) * fmaxf(ik[t >> 5], ik[s >> 5]));
+        }
+    }
+    m1 = absmax_bits(__float_as_uint(m1)), m2 = absmax_bits(__float_as_uint(m2)), m3 = absmax_bits(__float_as_uint(m3));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) pi += __shfl_xor_sync(0xffffffffu, pi, o);
+    if (lane == 0) wmax[0][warp] = m1, wmax[1][warp] = m2, wmax[2][warp] = m3, wpi[warp] = pi;
+    __syncthreads();
+    m1 = m2 = m3 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m1 = fmaxf(m1, wmax[0][i]), m2 = fmaxf(m2, wmax[1][i]), m3 = fmaxf(m3, wmax[2][i]);
+    float i1, i2, i3;
+    const float s1 = pow2_scale(m1, i1), s2 = pow2_scale(m2, i2), s3 = pow2_scale(m3, i3);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int sb = 2 * half + b;
+      if (sb > mt) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int t = r0 + 8 * hh, s = 16 * sb + 8 * i + 2 * (lane & 3);
+          const uint32_t o = tile_off<64>(t, s);
+          const float ks = ik[s >> 5], kt = ik[t >> 5], qt = iq[t >> 5];
+          const float pa = P[b][i][2 * hh], pb = P[b][i][2 * hh + 1], za = Z[b][i][2 * hh], zb = Z[b][i][2 * hh + 1];
+          const auto put = [&](int at, bool two, float2 x) {
+            uint32_t hi, lo;
+            split2(x, hi, lo);
+            *reinterpret_cast<uint32_t*>(sm + at + o) = hi;
+            if (two) *reinterpret_cast<uint32_t*>(sm + at + G::kSmall + o) = lo;
+          };
+          put(G::kW1, true, mul2(pa * ks, pb * ks, s1));
+          put(G::kW2, TM == 2, mul2(pa * qt, pb * qt, s2));
+          put(G::kZa, TM == 2, mul2(za * kt, zb * kt, s3));
+          put(G::kZb, TM == 2, mul2(za * ks, zb * ks, s3));
+        }
+    }
+    __syncthreads();
+    {
+      float tmp[TN][4];
+      const int nb = half * (NS / 2);
+      clear(tmp);
+      product<TN, 64, false, 2, NS, TM>(tmp, smu + G::kW1, G::kSmall, 16 * mt, smu + G::kK, G::kTok, nb, 0, mt + 1, lane);
+      add_rows(dqh, tmp, i1, i1);
+      clear(tmp);
+      product<TN, 64, true, TM, NS, TM>(tmp, smu + G::kW2, G::kSmall, 16 * mt, smu + G::kQ, G::kTok, nb, mt, 4, lane);
+      add_rows(dk, tmp, i2, i2);
+      clear(tmp);
+      product<TN, 64, true, TM, NS, TM>(tmp, smu + G::kZa, G::kSmall, 16 * mt, smu + G::kK, G::kTok, nb, mt, 4, lane);
+      product<TN, 64, false, TM, NS, TM>(tmp, smu + G::kZb, G::kSmall, 16 * mt, smu + G::kK, G::kTok, nb, 0, mt + 1, lane);
+      add_rows(dk, tmp, i3, i3);
+      // q.dq of this head
+      float q0 = 0.f, q1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint32_t o = tile_off<NS>(r0 + 8 * hh, nb + 8 * i + 2 * (lane & 3));
+          float2 q = unpack2(*reinterpret_cast<const uint32_t*>(sm + G::kQ + o));
+          if constexpr (TM == 2) {
+            const float2 l = unpack2(*reinterpret_cast<const uint32_t*>(sm + G::kQ + G::kTok + o));
+            q.x += l.x, q.y += l.y;
+          }
+          float& to = hh ? q1 : q0;
+          to = fmaf(q.x, dqh[i][2 * hh], fmaf(q.y, dqh[i][2 * hh + 1], to));
+        }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        q0 += __shfl_xor_sync(0xffffffffu, q0, o);
+        q1 += __shfl_xor_sync(0xffffffffu, q1, o);
+      }
+      q0 *= iq[r0 >> 5], q1 *= iq[(r0 + 8) >> 5];
+      if (half == 1 && (lane & 3) == 0) sums[2][r0] = q0, sums[2][r0 + 8] = q1;
+      __syncthreads();
+      if (half == 0 && (lane & 3) == 0) {
+        float* o = a.qdq + (int64_t)ns * a.part_stride + ((int64_t)sl.tok + r0) * a.H + h;
+        if (r0 < sl.n) o[0] = q0 + sums[2][r0];
+        if (r0 + 8 < sl.n) o[8 * a.H] = q1 + sums[2][r0 + 8];
+      }
+      add_rows(dq, dqh, 1.f, 1.f);
+    }
+    if (ns == 0 && threadIdx.x < sl.n) {
+      const int64_t o = ((int64_t)sl.tok + threadIdx.x) * a.H + h;
+      a.dbeta[o] = sums[0][threadIdx.x];
+      a.dvv[o] = sums[1][threadIdx.x] * bet[threadIdx.x];
+    }
+    if (threadIdx.x == 0) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += wpi[i];
+      a.pi[((int64_t)ns * a.slots_n + slot) * a.H + h] = s;
+    }
+  }
+  // dq and dk: rows of the group, or this split's part of them
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int t = r0 + 8 * hh, n = n0 + half * (NS / 2) + 8 * i + 2 * (lane & 3);
+        if (t >= sl.n || n >= a.N) continue;
+        const float x = (w ? dk : dq)[i][2 * hh], y = (w ? dk : dq)[i][2 * hh + 1];
+        const int64_t o = (((int64_t)sl.tok + t) * a.G + grp) * a.N + n;
+        if (a.splits > 1) {
+          float* d = a.part + (int64_t)(2 * split + w) * a.part_size + o;
+          d[0] = x;
+          if (n + 1 < a.N) d[1] = y;
+        } else {
+          T* d = static_cast<T*>(w ? a.dk : a.dq) + o;
+          if (n + 1 < a.N && a.pair) {
+            if constexpr (sizeof(T) == 2) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+              *reinterpret_cast<__nv_bfloat162*>(d) = b;
+            } else {
+              *reinterpret_cast<float2*>(d) = make_float2(x, y);
+            }
+          } else {
+            d[0] = from_f<T>(x);
+            if (n + 1 < a.N) d[1] = from_f<T>(y);
+          }
+        }
+      }
+}
+
+// dg: two threads take the 64 tokens of a slot and head, one the second half
+// from the end, one the first half from the start (or, where an initial state
+// comes in, all of it from the end).
+__global__ void __launch_bounds__(128) k_delta_dg(const GradArgs a, float* __restrict__ dg) {
+  const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+  const bool from_end = i < a.slots_n * a.H;
+  const int64_t j = from_end ? i : i - a.slots_n * a.H;
+  if (j >= a.slots_n * a.H) return;
+  const int64_t slot = j / a.H, h = j % a.H;
+  const Slot s = a.slots ? a.slots[slot] : row_slot(a, slot);
+  const bool start = s.h0 == kInside || s.h0 < 0 || !a.initial;  // <dS, S> before the slot is known
+  if (!from_end && !start) return;
+  const auto at_end = [&](int64_t of) {
+    float x = 0.f;
+    for (int c = 0; c < a.nslices; ++c) x += a.pi[(c * a.slots_n + of) * a.H + h];
+    return x;
+  };
+  const auto step = [&](int64_t o) {
+    float x = -a.dvv[o];
+    for (int c = 0; c < a.nslices; ++c) x += a.qdq[c * a.part_stride + o];
+    return x;
+  };
+  const int mid = start ? (s.n + 1) / 2 : 0;
+  if (from_end) {
+    float sum = at_end(slot);
+#pragma unroll 8
+    for (int t = s.n - 1; t >= mid; --t) {
+      const int64_t o = ((int64_t)s.tok + t) * a.H + h;
+      sum += step(o);
+      dg[o] = sum;
+    }
+  } else {
+    float sum = s.h0 == kInside && s.n > 0 ? at_end(slot - 1) : 0.f;
+#pragma unroll 8
+    for (int t = 0; t < mid; ++t) {
+      const int64_t o = ((int64_t)s.tok + t) * a.H + h;
+      dg[o] = sum;
+      sum -= step(o);
+    }
+  }
+}
+
+// dq and dk from the splits' parts, in order.
+template <typename T>
+__global__ void __launch_bounds__(256) k_delta_sum(const float* __restrict__ part, int splits, int64_t n, T* dq, T* dk) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float q = 0.f, k = 0.f;
+  for (int s = 0; s < splits; ++s) q += part[2 * s * n + i], k += part[(2 * s + 1) * n + i];
+  dq[i] = from_f<T>(q), dk[i] = from_f<T>(k);
+}
+
+template <typename T, int NT>
+cudaError_t launch_grads_nt(const GradArgs& a, cudaStream_t stream) {
+  constexpr int smem = GradTiles<T, NT>::kBytes;
+  static_assert(smem <= 220 * 1024, "shared memory");
+  const cudaError_t e = cudaFuncSetAttribute(k_delta_grads<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  k_delta_grads<T, NT><<<(unsigned)(a.slots_n * a.G * a.nslices * a.splits), kGradThreads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+int grad_slices(int64_t N) {
+  return N <= 64 ? 1 : N <= 128 ? 128 / GradTiles<T, 128>::kNS : 256 / GradTiles<T, 256>::kNS;
+}
+
+template <typename T>
+cudaError_t launch_grads(const GradArgs& a, float* dg, cudaStream_t stream) {
+  cudaError_t e = a.N <= 64    ? launch_grads_nt<T, 64>(a, stream)
+                  : a.N <= 128 ? launch_grads_nt<T, 128>(a, stream)
+                               : launch_grads_nt<T, 256>(a, stream);
+  if (e != cudaSuccess) return e;
+  k_delta_dg<<<(unsigned)((2 * a.slots_n * a.H + 127) / 128), 128, 0, stream>>>(a, dg);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.splits > 1) {
+    k_delta_sum<T><<<(unsigned)((a.part_size + 255) / 256), 256, 0, stream>>>(a.part, a.splits, a.part_size,
+                                                                             static_cast<T*>(a.dq), static_cast<T*>(a.dk));
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+}  // namespace delta
+}  // namespace ssd

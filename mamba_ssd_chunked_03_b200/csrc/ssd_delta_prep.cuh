@@ -42,7 +42,8 @@ struct alignas(16) Factors {
   float mu[kC];   // 1 / scale of the rows of M
   float beta[kC];
   float whole;    // exp(cs_C)
-  float pad[3];
+  float ik, iq;   // 1 / scale of the chunk's k and q tiles
+  float pad;
 };
 
 // Sizes of the images, in bytes.
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(const PrepArgs a) {
       f->kc[lane] = (rev ? outof : into) * inv_k;
       f->uc[lane] = (rev ? -into : outof) * bt * inv_k;
       f->beta[lane] = bt;
-      if (lane == 31) f->whole = into;
+      if (lane == 31) f->whole = into, f->ik = inv_k, f->iq = inv_q;
       if (rev || kFwdM) {
         row(gq, a.scale, 0, [&](int cidx, float w) { t[cidx] = w; });
         char* mi = img + (rev ? HR::kM : HF::kM);

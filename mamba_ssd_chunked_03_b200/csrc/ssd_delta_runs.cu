@@ -23,8 +23,13 @@ __device__ __forceinline__ bool starts(const int32_t* seq, int64_t i, int64_t L)
 }
 
 __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restrict__ seq, int64_t n, int64_t L,
-                                                         int64_t cap, int64_t places, Run* runs, Chunk* chunks,
-                                                         int32_t* first, int32_t* present) {
+                                                         int64_t cap, int64_t places, int64_t checks,
+                                                         const RunList out) {
+  Run* const runs = out.runs;
+  Chunk* const chunks = out.chunks;
+  Slot* const slots = out.slots;
+  int32_t* const first = out.first;
+  int32_t* const present = out.present;
   __shared__ int warp_count[32];
   __shared__ int total, absent;
   __shared__ int lens[kRanked];
@@ -36,6 +41,7 @@ __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restri
     runs[i] = r;
   }
   for (int64_t i = threadIdx.x; i < places; i += kThreads) chunks[i] = Chunk{0, 0};
+  for (int64_t i = threadIdx.x; i < checks; i += kThreads) slots[i] = Slot{0, 0, 0, kInside, kInside};
   const int64_t per = ((n + 31) / 32 + 31) / 32 * 32;  // ids per warp, a multiple of 32
   const int64_t i0 = warp * per, i1 = i0 + per < n ? i0 + per : n;
   int count = 0;
@@ -104,6 +110,12 @@ __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restri
     const int t = first[k], len = ranked ? lens[k] : len_of(k);
     for (int i = lane * kC; i < len; i += 32 * kC)
       chunks[t / kC + k + i / kC] = Chunk{t + i, len - i < kC ? len - i : kC};
+    const int id = seq[t];
+    for (int i = lane * kCheck; i < len; i += 32 * kCheck)
+      slots[t / kCheck + k + i / kCheck] =
+          Slot{t + i, len - i < kCheck ? len - i : kCheck, (int)(t / kC + k + i / kC),
+               i + kCheck < len ? kInside : id >= 0 && id < cap ? id : -1,
+               i > 0 ? kInside : t % L == 0 ? (int)(t / L) : -1};
   }
   __syncthreads();
   for (int64_t i = threadIdx.x; i < cap; i += kThreads) {
@@ -118,6 +130,7 @@ __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restri
 size_t runs_bytes(const Shape& s) {
   if (!s.packed) return 0;
   return align_up((size_t)s.runs * sizeof(Run), kWsAlign) + align_up((size_t)s.chunks * sizeof(Chunk), kWsAlign) +
+         align_up((size_t)s.slots * sizeof(Slot), kWsAlign) +
          2 * align_up((size_t)(s.runs + 1) * 4, kWsAlign);
 }
 
@@ -129,6 +142,8 @@ RunList runs_at(const Shape& s, void* ws) {
   p += align_up((size_t)s.runs * sizeof(Run), kWsAlign);
   r.chunks = reinterpret_cast<Chunk*>(p);
   p += align_up((size_t)s.chunks * sizeof(Chunk), kWsAlign);
+  r.slots = reinterpret_cast<Slot*>(p);
+  p += align_up((size_t)s.slots * sizeof(Slot), kWsAlign);
   r.first = reinterpret_cast<int32_t*>(p);
   p += align_up((size_t)(s.runs + 1) * 4, kWsAlign);
   r.present = reinterpret_cast<int32_t*>(p);
@@ -136,7 +151,7 @@ RunList runs_at(const Shape& s, void* ws) {
 }
 
 cudaError_t launch_runs(const Shape& s, const int32_t* seq, const RunList& r, cudaStream_t stream) {
-  k_delta_runs<<<1, kThreads, 0, stream>>>(seq, s.b * s.L, s.L, s.runs, s.chunks, r.runs, r.chunks, r.first, r.present);
+  k_delta_runs<<<1, kThreads, 0, stream>>>(seq, s.b * s.L, s.L, s.runs, s.chunks, s.slots, r);
   return cudaGetLastError();
 }
 

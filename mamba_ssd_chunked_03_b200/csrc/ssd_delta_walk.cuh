@@ -31,6 +31,10 @@ struct WalkArgs {
   void* out;           // forward: y; state walk: E (fp32); reverse: dv
   float* out_f;        // reverse: D (fp32)
   float* check;        // state at every 64th token of a run (state walk, reverse)
+  float* max_v;        // largest magnitude of each 16 rows of V in each chunk (reverse), of
+  float* max_out;      // E or D there, and of the state at each checkpoint: [.][head][pg],
+  float* max_check;    // for the kernel that turns them into operands
+  int pg;              // sixteens of headdim
   float* fin;          // final state (forward) or gradient of the initial state (reverse), or null
   int v_vec, out_vec;  // rows start on 16-byte boundaries
 };
@@ -224,6 +228,17 @@ __device__ __forceinline__ void load_v(float (&v)[4][4], const char* tile, int p
   }
 }
 
+// The largest magnitude of a thread's tile, and of the warp's.
+__device__ __forceinline__ float tile_max(const float (&x)[4][4]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(x[i][e]));
+  return m;
+}
+__device__ __forceinline__ float warp_absmax(float m) { return absmax_bits(__float_as_uint(m)); }
+
 __device__ __forceinline__ void zero(float (&x)[4][4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -314,6 +329,26 @@ __device__ __forceinline__ void lower_mma(float (&d)[4][4], const uint32_t (&hi)
   }
 }
 
+// d (p x s) += X (p x t) W for a lower triangular 32 x 32 tile W (t x s).
+template <bool XLO>
+__device__ __forceinline__ void lower_mma_t(float (&d)[4][4], const uint32_t (&hi)[2][4], const uint32_t (&lo)[2][4],
+                                            uint32_t tile, int lane) {
+  const int tr = (lane & 7) + ((lane >> 3) & 1) * 8, nc = (lane >> 4) * 8;
+  uint32_t B[3][4];  // (t, s) blocks of 16: (1, 0), (1, 1), (0, 0)
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+      ldsm4t(tile + w * kSq + tile_off<32>(16 * (x < 2) + tr, 16 * (x == 1) + nc), B[x]);
+#pragma unroll
+    for (int x = 0; x < 6; ++x) mma(d[x & 3], hi[x < 4], B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
+    if (XLO && w == 0) {
+#pragma unroll
+      for (int x = 0; x < 6; ++x) mma(d[x & 3], lo[x < 4], B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
+    }
+  }
+}
+
 template <typename T, int NT, int MODE>
 __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(const WalkArgs a) {
   constexpr bool kY = MODE == kForward;
@@ -362,12 +397,16 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(cons
     const Factors& f = *reinterpret_cast<const Factors*>(buf + B::kHead + Hd::kF);
     const uint32_t kt = sm100::smem_u32(buf), qt = kt + kTerms * X::kTile;
     const uint32_t tt = kt + B::kHead, mt = tt + Hd::kM;
-    if constexpr (MODE == kStates) {
-      if ((j & 1) == 0)
-        store_state<NT>(S, sig0, sig1, a.check + (((run.slot + (j >> 1)) * a.H + h) * a.P + p0) * a.N, a.N, rows, lane);
-    }
     float m0, m1, inv0, inv1;
     state_max<NT>(S, m0, m1);
+    if constexpr (MODE == kStates) {
+      if ((j & 1) == 0) {
+        const int64_t at = (run.slot + (j >> 1)) * a.H + h;
+        store_state<NT>(S, sig0, sig1, a.check + (at * a.P + p0) * a.N, a.N, rows, lane);
+        const float m = warp_absmax(fmaxf(m0 * sig0, m1 * sig1));
+        if (lane == 0) a.max_check[at * a.pg + p0 / 16] = m;
+      }
+    }
     const float sc0 = pow2_scale(m0, inv0), sc1 = pow2_scale(m1, inv1);
     inv0 *= sig0, inv1 *= sig1;
     float acc[4][4], yq[4][4];
@@ -424,6 +463,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(cons
       store_tile<T>(yq, stage, static_cast<T*>(a.out) + row0, a.H * a.P, n, rows, a.out_vec, lane);
     } else {
       store_tile<float>(e, stage, static_cast<float*>(a.out) + row0, a.H * a.P, n, rows, a.out_vec, lane);
+      const float m = warp_absmax(tile_max(e));
+      if (lane == 0) a.max_out[((run.chunk + j) * a.H + h) * a.pg + p0 / 16] = m;
     }
     // S' = exp(cs_C) S + U K, in units in which U fills fp16's range and S stays below 2^35
     float u0 = 0.f, u1 = 0.f;

@@ -794,23 +794,26 @@ def causal_conv1d_silu(u: torch.Tensor, weight: torch.Tensor, bias: Optional[tor
     return _CausalConv1dSilu.apply(u, weight, bias, seq_idx)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # a tenth of the cost of building a Stream object
+
+
 def _call(entry, args, device: torch.device) -> None:
     """Run a library entry point on the current stream of ``device``, which is
     made the current device for the call if it is not."""
     index = device.index
     if index == torch.cuda.current_device():
-        st = entry(ctypes.byref(args), torch.cuda.current_stream(index).cuda_stream)
+        st = entry(args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            st = entry(ctypes.byref(args), torch.cuda.current_stream(index).cuda_stream)
+            st = entry(args, _raw_stream(index))
     if st != SSD_OK:
         raise SSDError(st)
 
 
-def _check_tensors(dev: torch.device, named) -> None:
+def _check_tensors(dev: torch.device, **named) -> None:
     if dev.type != "cuda":
         raise ValueError("the tensors must be CUDA tensors")
-    for name, t in named:
+    for name, t in named.items():
         if t is not None and (t.device != dev or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
 
@@ -831,18 +834,19 @@ def _check_delta(q, k, v, g, beta, initial_states, seq_idx):
         raise ValueError("initial_states must be float32 (b, H, P, N)")
     if seq_idx is not None and (seq_idx.dtype != torch.int32 or tuple(seq_idx.shape) != (b, L)):
         raise ValueError("seq_idx must be int32 (b, L)")
-    _check_tensors(v.device, (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta),
-                              ("initial_states", initial_states), ("seq_idx", seq_idx)))
+    _check_tensors(v.device, q=q, k=k, v=v, g=g, beta=beta, initial_states=initial_states, seq_idx=seq_idx)
 
 
-def _fill_delta(a, q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs) -> None:
-    a.batch, a.seqlen, a.nheads, a.headdim = v.shape
-    a.ngroups, a.dstate = q.shape[2], q.shape[3]
-    a.dtype = SSD_BF16 if v.dtype == torch.bfloat16 else SSD_F32
-    a.q, a.k, a.v, a.g, a.beta = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr()
-    a.initial_states, a.seq_idx = _ptr(initial_states), _ptr(seq_idx)
-    a.num_seqs = int(num_seqs) if seq_idx is not None else 0
-    a.scale = float(a.dstate ** -0.5 if scale is None else scale)
+def _dtype(t: torch.Tensor) -> int:
+    return SSD_BF16 if t.dtype == torch.bfloat16 else SSD_F32
+
+
+def _delta_args(q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs, flags=0) -> DeltaArgs:
+    b, L, H, P = v.shape
+    G, N = q.shape[2:]
+    return DeltaArgs(b, L, H, P, N, G, _dtype(v), flags, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                     beta.data_ptr(), _ptr(initial_states), _ptr(seq_idx), int(num_seqs) if seq_idx is not None else 0,
+                     None, None, None, 0, N ** -0.5 if scale is None else scale)
 
 
 def _workspace(workspace: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
@@ -853,6 +857,10 @@ def _workspace(workspace: Optional[torch.Tensor], need: int, device) -> torch.Te
         if workspace.numel() * workspace.element_size() >= need:
             return workspace
     return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def _output_like(out: Optional[torch.Tensor], name: str, t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t) if out is None else _output(out, name, t.shape, t.dtype, t.device)
 
 
 def _output(out: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
@@ -885,17 +893,15 @@ def delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
     b, L, H, P = v.shape
     if seq_idx is not None and num_seqs is None:
         num_seqs = int(seq_idx.max().item()) + 1
-    y = _output(y, "y", v.shape, v.dtype, v.device)
+    y = _output_like(y, "y", v)
     if return_final_states:
         final_states = _output(final_states, "final_states",
                                (num_seqs if seq_idx is not None else b, H, P, q.shape[3]), torch.float32, v.device)
     else:
         final_states = None
-    a = DeltaArgs()
-    _fill_delta(a, q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs)
-    a.flags = SSD_FLAG_CHECK_SEQ if check_seq else 0
+    a = _delta_args(q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs, SSD_FLAG_CHECK_SEQ if check_seq else 0)
     a.y, a.final_states = y.data_ptr(), _ptr(final_states)
-    need = int(lib.ssd_delta_fwd_workspace_size(ctypes.byref(a)))
+    need = int(lib.ssd_delta_fwd_workspace_size(a))
     if need:
         workspace = _workspace(workspace, need, v.device)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -924,19 +930,16 @@ def delta_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
     if dfinal_states is not None and (dfinal_states.dtype != torch.float32
                                       or tuple(dfinal_states.shape) != (rows, H, P, N)):
         raise ValueError(f"dfinal_states must be float32 {(rows, H, P, N)}")
-    _check_tensors(v.device, (("dy", dy), ("dfinal_states", dfinal_states)))
+    _check_tensors(v.device, dy=dy, dfinal_states=dfinal_states)
     if want_dinitial_states is None:
         want_dinitial_states = initial_states is not None
     d = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v), "dg": torch.empty_like(g),
          "dbeta": torch.empty_like(beta),
          "dinitial_states": torch.empty(b, H, P, N, device=v.device, dtype=torch.float32)
          if want_dinitial_states else None}
-    a = DeltaBwdArgs()
-    _fill_delta(a.fwd, q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs)
-    a.dy, a.dfinal_states = dy.data_ptr(), _ptr(dfinal_states)
-    a.dq, a.dk, a.dv, a.dg, a.dbeta, a.dinitial_states = (_ptr(d[n]) for n in (
-        "dq", "dk", "dv", "dg", "dbeta", "dinitial_states"))
-    need = int(lib.ssd_delta_bwd_workspace_size(ctypes.byref(a)))
+    a = DeltaBwdArgs(_delta_args(q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs), dy.data_ptr(),
+                     _ptr(dfinal_states), *(_ptr(t) for t in d.values()))
+    need = int(lib.ssd_delta_bwd_workspace_size(a))
     if need:
         workspace = _workspace(workspace, need, v.device)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -993,14 +996,10 @@ def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
         raise TypeError("q, k and v must all be float32 or all bfloat16")
     if g.dtype != torch.float32 or beta.dtype != torch.float32 or state.dtype != torch.float32:
         raise TypeError("g, beta and state must be float32")
-    _check_tensors(v.device, (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("state", state)))
-    y = _output(y, "y", v.shape, v.dtype, v.device)
-    a = DeltaStepArgs()
-    a.batch, a.nheads, a.headdim, a.dstate, a.ngroups = b, H, P, N, G
-    a.dtype = SSD_BF16 if v.dtype == torch.bfloat16 else SSD_F32
-    a.scale = float(N ** -0.5 if scale is None else scale)
-    a.q, a.k, a.v, a.g, a.beta = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr()
-    a.state, a.y = state.data_ptr(), y.data_ptr()
+    _check_tensors(v.device, q=q, k=k, v=v, g=g, beta=beta, state=state)
+    y = _output_like(y, "y", v)
+    a = DeltaStepArgs(b, H, P, N, G, _dtype(v), N ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(),
+                      v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), y.data_ptr())
     _call(lib.ssd_delta_step, a, v.device)
     return y
 
@@ -1011,12 +1010,13 @@ def _check_norm(x, weight, bias, z) -> None:
     if x.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("x must be float32 or bfloat16")
     cols = x.shape[-1]
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (cols,)):
-            raise ValueError(f"{name} must be float32 ({cols},)")
+    if weight is not None and (weight.dtype != torch.float32 or weight.shape != (cols,)):
+        raise ValueError(f"weight must be float32 ({cols},)")
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (cols,)):
+        raise ValueError(f"bias must be float32 ({cols},)")
     if z is not None and (z.dtype != x.dtype or z.shape != x.shape):
         raise ValueError("z must be like x")
-    _check_tensors(x.device, (("x", x), ("weight", weight), ("bias", bias), ("z", z)))
+    _check_tensors(x.device, x=x, weight=weight, bias=bias, z=z)
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -1025,13 +1025,10 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     axis of x (..., D) fp32|bf16, weight and bias (D) fp32 or None, the gate z
     like x or None (then without SiLU(z)).  ``out`` may be x or z itself."""
     _check_norm(x, weight, bias, z)
-    out = _output(out, "out", x.shape, x.dtype, x.device)
-    a = NormArgs()
-    a.cols = x.shape[-1]
-    a.rows = x.numel() // a.cols if a.cols else 0
-    a.dtype = SSD_BF16 if x.dtype == torch.bfloat16 else SSD_F32
-    a.eps = eps
-    a.x, a.weight, a.bias, a.z, a.out = x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(z), out.data_ptr()
+    out = _output_like(out, "out", x)
+    cols = x.shape[-1]
+    a = NormArgs(x.numel() // cols if cols else 0, cols, _dtype(x), eps, x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(z),
+                 out.data_ptr())
     _call(lib.ssd_layer_norm, a, x.device)
     return out
 
@@ -1046,7 +1043,7 @@ def layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Option
     _check_norm(x, weight, bias, z)
     if dout.dtype != x.dtype or dout.shape != x.shape:
         raise ValueError("dout must be like x")
-    _check_tensors(x.device, (("dout", dout),))
+    _check_tensors(x.device, dout=dout)
     cols = x.shape[-1]
     want_dweight = weight is not None if want_dweight is None else want_dweight
     want_dbias = bias is not None if want_dbias is None else want_dbias
@@ -1054,14 +1051,9 @@ def layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Option
     dw = torch.empty(cols, device=x.device, dtype=torch.float32) if want_dweight else None
     db = torch.empty(cols, device=x.device, dtype=torch.float32) if want_dbias else None
     dz = torch.empty_like(x) if z is not None else None
-    a = NormBwdArgs()
-    a.cols = cols
-    a.rows = x.numel() // cols if cols else 0
-    a.dtype = SSD_BF16 if x.dtype == torch.bfloat16 else SSD_F32
-    a.eps = eps
-    a.x, a.weight, a.bias, a.z, a.dout = x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(z), dout.data_ptr()
-    a.dx, a.dweight, a.dbias, a.dz = dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(dz)
-    need = int(lib.ssd_layer_norm_bwd_workspace_size(ctypes.byref(a)))
+    a = NormBwdArgs(x.numel() // cols if cols else 0, cols, _dtype(x), eps, x.data_ptr(), _ptr(weight), _ptr(bias), _ptr(z),
+                    dout.data_ptr(), dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(dz))
+    need = int(lib.ssd_layer_norm_bwd_workspace_size(a))
     ws = torch.empty(need, dtype=torch.uint8, device=x.device)
     a.workspace, a.workspace_bytes = ws.data_ptr(), need
     _call(lib.ssd_layer_norm_bwd, a, x.device)

@@ -502,45 +502,46 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
       }
 }
 
-// dg: two threads take the 64 tokens of a slot and head, one the second half
-// from the end, one the first half from the start (or, where an initial state
+// dg: a warp takes the 64 tokens of a slot and head, two a lane; the second
+// half from the end, the first half from the start (or, where an initial state
 // comes in, all of it from the end).
-__global__ void __launch_bounds__(128) k_delta_dg(const GradArgs a, float* __restrict__ dg) {
-  const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
-  const bool from_end = i < a.slots_n * a.H;
-  const int64_t j = from_end ? i : i - a.slots_n * a.H;
-  if (j >= a.slots_n * a.H) return;
-  const int64_t slot = j / a.H, h = j % a.H;
+__global__ void __launch_bounds__(256) k_delta_dg(const GradArgs a, float* __restrict__ dg) {
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= a.slots_n * a.H) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t slot = i / a.H, h = i % a.H;
   const Slot s = a.slots ? a.slots[slot] : row_slot(a, slot);
+  if (s.n == 0) return;
   const bool start = s.h0 == kInside || s.h0 < 0 || !a.initial;  // <dS, S> before the slot is known
-  if (!from_end && !start) return;
-  const auto at_end = [&](int64_t of) {
-    float x = 0.f;
-    for (int c = 0; c < a.nslices; ++c) x += a.pi[(c * a.slots_n + of) * a.H + h];
-    return x;
-  };
-  const auto step = [&](int64_t o) {
-    float x = -a.dvv[o];
-    for (int c = 0; c < a.nslices; ++c) x += a.qdq[c * a.part_stride + o];
-    return x;
-  };
+  float x[2], before = 0.f, after = 0.f;  // tokens 2 lane, 2 lane + 1: dq.q - dv.v
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int t = 2 * lane + e;
+    const int64_t o = ((int64_t)s.tok + t) * a.H + h;
+    x[e] = t < s.n ? -a.dvv[o] : 0.f;
+    if (t < s.n)
+      for (int c = 0; c < a.nslices; ++c) x[e] += a.qdq[c * a.part_stride + o];
+  }
+  for (int c = 0; c < a.nslices; ++c) {
+    after += a.pi[(c * a.slots_n + slot) * a.H + h];
+    if (s.h0 == kInside) before += a.pi[(c * a.slots_n + slot - 1) * a.H + h];
+  }
+  float up = x[0] + x[1], down = up;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float u = __shfl_up_sync(0xffffffffu, up, o), d = __shfl_down_sync(0xffffffffu, down, o);
+    if (lane >= o) up += u;
+    if (lane + o < 32) down += d;
+  }
+  // sums over the tokens before this lane's, and from this lane's on
+  const float upto = __shfl_up_sync(0xffffffffu, up, 1), from = down;
   const int mid = start ? (s.n + 1) / 2 : 0;
-  if (from_end) {
-    float sum = at_end(slot);
-#pragma unroll 8
-    for (int t = s.n - 1; t >= mid; --t) {
-      const int64_t o = ((int64_t)s.tok + t) * a.H + h;
-      sum += step(o);
-      dg[o] = sum;
-    }
-  } else {
-    float sum = s.h0 == kInside && s.n > 0 ? at_end(slot - 1) : 0.f;
-#pragma unroll 8
-    for (int t = 0; t < mid; ++t) {
-      const int64_t o = ((int64_t)s.tok + t) * a.H + h;
-      dg[o] = sum;
-      sum -= step(o);
-    }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int t = 2 * lane + e;
+    if (t >= s.n) continue;
+    const float b = before - ((lane ? upto : 0.f) + (e ? x[0] : 0.f)), f = after + (e ? from - x[0] : from);
+    dg[((int64_t)s.tok + t) * a.H + h] = t < mid ? b : f;
   }
 }
 
@@ -575,7 +576,7 @@ cudaError_t launch_grads(const GradArgs& a, float* dg, cudaStream_t stream) {
                   : a.N <= 128 ? launch_grads_nt<T, 128>(a, stream)
                                : launch_grads_nt<T, 256>(a, stream);
   if (e != cudaSuccess) return e;
-  k_delta_dg<<<(unsigned)((2 * a.slots_n * a.H + 127) / 128), 128, 0, stream>>>(a, dg);
+  k_delta_dg<<<(unsigned)((a.slots_n * a.H + 7) / 8), 256, 0, stream>>>(a, dg);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (a.splits > 1) {
     k_delta_sum<T><<<(unsigned)((a.part_size + 255) / 256), 256, 0, stream>>>(a.part, a.splits, a.part_size,

@@ -25,8 +25,9 @@ namespace ssd {
 namespace {
 
 constexpr int kSMs = 148;
-constexpr int kThreads = 256;     // CTA of the row kernels
-constexpr int kParts = 2 * kSMs;  // CTAs of the backward, each with its partial sums
+constexpr int kThreads = 256;     // CTA of the kernels whose rows share one
+constexpr int kMostThreads = 512;  // CTA of one row, as many as it needs
+constexpr int kParts = 3 * kSMs;  // most CTAs of the backward, each with its partial sums
 
 struct Args {
   int64_t rows, cols;
@@ -93,47 +94,55 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + expf(-v)); }
-// z sigmoid(z), 0 at z = -inf
-__device__ __forceinline__ float silu(float v) { return v == -INFINITY ? 0.f : v * sigmoid(v); }
+// The hardware exponential and an approximate divide: off by a few 2^-23.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+// z sigmoid(z); 0 at z = -inf
+__device__ __forceinline__ float silu(float v) { return v < -1e30f ? 0.f : v * sigmoid(v); }
 
-// Sums over the GT threads of a group, the same bits in each of them.
+// Sums of N values over the GT threads of a group (GT > 32: the CTA's threads,
+// however many), the same bits in each of them.
 template <int GT>
 struct GroupSum {
-  float2 (*red)[kThreads / 32];  // two sets, taken in turn: one barrier a sum
+  float4 (*red)[kMostThreads / 32];  // two sets, taken in turn: one barrier a sum
   int turn = 0;
-  __device__ __forceinline__ float2 operator()(float a, float b) {
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
 #pragma unroll
-    for (int o = (GT < 32 ? GT : 32) / 2; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
+    for (int o = (GT < 32 ? GT : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     if constexpr (GT > 32) {
-      if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = make_float2(a, b);
+      if ((threadIdx.x & 31) == 0)
+        red[turn][threadIdx.x >> 5] = make_float4(v[0], v[N > 1 ? 1 : 0], v[N > 2 ? 2 : 0], v[N > 3 ? 3 : 0]);
       __syncthreads();
-      a = b = 0.f;
 #pragma unroll
-      for (int w = 0; w < GT / 32; ++w) {
-        const float2 v = red[turn][w];
-        a += v.x, b += v.y;
+      for (int i = 0; i < N; ++i) v[i] = 0.f;
+#pragma unroll 4
+      for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+        const float4 x = red[turn][w];
+        v[0] += x.x;
+        if constexpr (N > 1) v[1] += x.y;
+        if constexpr (N > 2) v[2] += x.z;
+        if constexpr (N > 3) v[3] += x.w;
       }
       turn ^= 1;
     }
-    return make_float2(a, b);
   }
 };
 
-// Rows held in registers: VPL packs of E elements a thread.
-template <typename T, int E, int GT, int VPL, bool BWD, bool GATE>
-__global__ void __launch_bounds__(kThreads) k_norm(const Args a) {
+// Rows held in registers: VPL packs of E elements for each of the GT threads of
+// a row (GT > 32: the CTA's threads, however many up to BT).
+template <typename T, int E, int GT, int VPL, int BT, int MINB, bool BWD, bool GATE>
+__global__ void __launch_bounds__(BT, MINB) k_norm(const Args a) {
   using Pk = Pack<T, E>;
-  constexpr int GC = kThreads / GT;  // groups of a CTA
-  __shared__ float2 red[2][kThreads / 32];
+  constexpr int GC = GT > 32 ? 1 : kThreads / GT;  // groups of a CTA
+  __shared__ float4 red[2][kMostThreads / 32];
   GroupSum<GT> sum{red};
-  const int g = threadIdx.x / GT, l = threadIdx.x % GT;
+  const int gt = GT > 32 ? blockDim.x : GT;  // threads of a row
+  const int g = GT > 32 ? 0 : threadIdx.x / GT, l = GT > 32 ? threadIdx.x : threadIdx.x % GT;
   const int64_t cols = a.cols;
   const float inv_cols = 1.f / (float)cols;
-  const auto col = [&](int v) { return (int64_t)(v * GT + l) * E; };
+  const auto col = [&](int v) { return (int64_t)(v * gt + l) * E; };
   float w[VPL][E], b[VPL][E], dw[VPL][E], db[VPL][E];
 #pragma unroll
   for (int v = 0; v < VPL; ++v)
@@ -160,8 +169,8 @@ __global__ void __launch_bounds__(kThreads) k_norm(const Args a) {
   for (int64_t r0 = (int64_t)blockIdx.x * GC; r0 < a.rows; r0 += stride) {  // the same trips for all threads
     const int64_t r = r0 + g;
     const bool live = r < a.rows;
-    float x[VPL][E], z[VPL][E], d[VPL][E];
-    float s = 0.f;
+    float x[VPL][E], z[VPL][E], d[VPL][E];  // x - mean, the gate, and dout: then dout SiLU(z)
+    float s0[1] = {0.f}, sq[1] = {0.f};
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       const bool in = live && col(v) < cols;
@@ -170,21 +179,24 @@ __global__ void __launch_bounds__(kThreads) k_norm(const Args a) {
       if constexpr (BWD) dr[v].get(d[v]);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        if (!in) x[v][e] = 0.f, z[v][e] = 0.f, d[v][e] = 0.f;
-        s += x[v][e];
+        x[v][e] = in ? x[v][e] : 0.f;
+        if constexpr (GATE) z[v][e] = in ? z[v][e] : 0.f;
+        if constexpr (BWD) d[v][e] = in ? d[v][e] : 0.f;
+        s0[0] += x[v][e];
       }
     }
     fetch(r + stride);
-    const float mean = sum(s, 0.f).x * inv_cols;
-    s = 0.f;
+    sum(s0);
+    const float mean = s0[0] * inv_cols;
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         x[v][e] = col(v) < cols ? x[v][e] - mean : 0.f;
-        s = fmaf(x[v][e], x[v][e], s);
+        sq[0] = fmaf(x[v][e], x[v][e], sq[0]);
       }
-    const float rstd = 1.f / sqrtf(fmaf(sum(s, 0.f).x, inv_cols, a.eps));
+    sum(sq);
+    const float rstd = 1.f / sqrtf(fmaf(sq[0], inv_cols, a.eps));
     if constexpr (!BWD) {
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
@@ -197,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) k_norm(const Args a) {
         if (live && col(v) < cols) Pk::store(static_cast<T*>(a.out) + r * cols + col(v), y);
       }
     } else {
-      float s1 = 0.f, s2 = 0.f;
+      float m[2] = {0.f, 0.f};
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
         float dz[E];
@@ -212,21 +224,20 @@ __global__ void __launch_bounds__(kThreads) k_norm(const Args a) {
           }
           dw[v][e] = fmaf(h, n, dw[v][e]);
           db[v][e] += h;
-          const float hw = h * w[v][e];
-          s1 += hw;
-          s2 = fmaf(hw, n, s2);
-          x[v][e] = n, d[v][e] = hw;
+          d[v][e] = h * w[v][e];
+          m[0] += d[v][e];
+          m[1] = fmaf(d[v][e], n, m[1]);
         }
         if constexpr (GATE)
           if (live && col(v) < cols) Pk::store(static_cast<T*>(a.dz) + r * cols + col(v), dz);
       }
-      const float2 m = sum(s1, s2);
-      const float m1 = m.x * inv_cols, m2 = m.y * inv_cols;
+      sum(m);
+      const float m1 = m[0] * inv_cols, m2 = m[1] * inv_cols * rstd;
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
         float y[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = rstd * (d[v][e] - m1 - x[v][e] * m2);
+        for (int e = 0; e < E; ++e) y[e] = rstd * (fmaf(-x[v][e], m2, d[v][e]) - m1);
         if (live && col(v) < cols) Pk::store(static_cast<T*>(a.out) + r * cols + col(v), y);
       }
     }
@@ -273,24 +284,168 @@ __global__ void __launch_bounds__(kThreads) k_norm(const Args a) {
   }
 }
 
+// Rows of bf16 that take a CTA.
+//
+// Such a row costs a barrier for every sum that waits for another one, so all
+// of its sums are taken at once, of the differences to K, the mean of the
+// row's first pack: x - mean = (x - K) - mean(x - K), var = mean((x - K)^2) -
+// mean(x - K)^2.  K is off the mean by at most sqrt(cols / 8) deviations, since
+// its elements are part of the row, and by less than one in all but contrived
+// rows; what cancels in var is then cols / 8 x 2^-24 at the very most, far
+// below the rounding of the outputs.  The row stays packed in registers and is
+// unpacked again after the sums; weight and bias lie in shared memory: that
+// leaves room for a second CTA's rows.
+template <int VPL, int BT, int MINB, bool BWD, bool GATE>
+__global__ void __launch_bounds__(BT, MINB) k_norm_row(const Args a) {
+  using T = __nv_bfloat16;
+  constexpr int E = 8;
+  using Pk = Pack<T, E>;
+  extern __shared__ __align__(16) float wb[];  // weight, bias
+  __shared__ float4 red[2][kMostThreads / 32];
+  GroupSum<64> sum{red};
+  const int l = threadIdx.x, gt = blockDim.x, cols = (int)a.cols;
+  const float inv_cols = 1.f / (float)cols;
+  const auto col = [&](int v) { return (v * gt + l) * E; };
+  for (int c = l; c < cols; c += gt) {
+    wb[c] = a.w ? a.w[c] : 1.f;
+    if constexpr (GATE || !BWD) wb[cols + c] = a.b ? a.b[c] : 0.f;
+  }
+  __syncthreads();
+  const auto weights = [&](int c, float (&w)[E]) {
+    const float4 p = *reinterpret_cast<const float4*>(wb + c), q = *reinterpret_cast<const float4*>(wb + c + 4);
+    w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w, w[4] = q.x, w[5] = q.y, w[6] = q.z, w[7] = q.w;
+  };
+  float dw[BWD ? VPL : 1][E], db[BWD ? VPL : 1][E];
+#pragma unroll
+  for (int v = 0; v < (BWD ? VPL : 1); ++v)
+#pragma unroll
+    for (int e = 0; e < E; ++e) dw[v][e] = db[v][e] = 0.f;
+  Pk xn[VPL], zn[VPL], dn[VPL], kn;
+  const auto fetch = [&](int64_t r) {
+    if (r >= a.rows) return;
+    const int64_t o = r * cols;
+    kn.load(static_cast<const T*>(a.x) + o);
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+      if (col(v) < cols) {
+        xn[v].load(static_cast<const T*>(a.x) + o + col(v));
+        if constexpr (GATE) zn[v].load(static_cast<const T*>(a.z) + o + col(v));
+        if constexpr (BWD) dn[v].load(static_cast<const T*>(a.dout) + o + col(v));
+      }
+  };
+  fetch(blockIdx.x);
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    Pk xr[VPL], zr[VPL], dr[VPL];
+    float K = 0.f;
+    {
+      float k[E];
+      kn.get(k);
+#pragma unroll
+      for (int e = 0; e < E; ++e) K += k[e];
+      K *= 1.f / E;
+    }
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      xr[v] = xn[v];
+      if constexpr (GATE) zr[v] = zn[v];
+      if constexpr (BWD) dr[v] = dn[v];
+    }
+    fetch(r + gridDim.x);
+    float t[BWD ? 4 : 2] = {};
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      if (col(v) >= cols) continue;
+      float x[E], d[E], z[E], w[E];
+      xr[v].get(x);
+      if constexpr (BWD) {
+        dr[v].get(d);
+        weights(col(v), w);
+      }
+      if constexpr (BWD && GATE) zr[v].get(z);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        x[e] -= K;
+        t[0] += x[e];
+        t[1] = fmaf(x[e], x[e], t[1]);
+        if constexpr (BWD) {
+          float h = d[e] * w[e];
+          if constexpr (GATE) h *= z[e] * sigmoid(z[e]);
+          t[2] += h;
+          t[3] = fmaf(h, x[e], t[3]);
+        }
+      }
+    }
+    sum(t);
+    const float dm = t[0] * inv_cols, mean = K + dm;
+    const float rstd = 1.f / sqrtf(fmaxf(fmaf(t[1], inv_cols, -dm * dm), 0.f) + a.eps);
+    float m1 = 0.f, m2 = 0.f;
+    if constexpr (BWD) m1 = t[2] * inv_cols, m2 = rstd * (t[3] - dm * t[2]) * inv_cols;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      if (col(v) >= cols) continue;
+      float x[E], d[E], z[E], w[E], b[E], dz[E];
+      xr[v].get(x);
+      if constexpr (BWD) dr[v].get(d);
+      if constexpr (GATE) zr[v].get(z);
+      weights(col(v), w);
+      if constexpr (GATE || !BWD) weights(cols + col(v), b);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float n = (x[e] - mean) * rstd;
+        if constexpr (!BWD) {
+          x[e] = fmaf(n, w[e], b[e]);
+          if constexpr (GATE) x[e] *= silu(z[e]);
+        } else {
+          float h = d[e];
+          if constexpr (GATE) {
+            const float sg = sigmoid(z[e]);
+            dz[e] = h * fmaf(n, w[e], b[e]) * (sg * fmaf(z[e], 1.f - sg, 1.f));
+            h *= z[e] * sg;
+          }
+          dw[v][e] = fmaf(h, n, dw[v][e]);
+          db[v][e] += h;
+          x[e] = rstd * (fmaf(-n, m2, h * w[e]) - m1);
+        }
+      }
+      Pk::store(static_cast<T*>(a.out) + r * cols + col(v), x);
+      if constexpr (BWD && GATE) Pk::store(static_cast<T*>(a.dz) + r * cols + col(v), dz);
+    }
+  }
+  if constexpr (BWD) {
+    if (!a.part) return;
+    float* pw = a.part + (int64_t)blockIdx.x * cols;
+    float* pb = pw + (int64_t)kParts * cols;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+      if (col(v) < cols) {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+          *reinterpret_cast<float4*>(pw + col(v) + e) = make_float4(dw[v][e], dw[v][e + 1], dw[v][e + 2], dw[v][e + 3]);
+          *reinterpret_cast<float4*>(pb + col(v) + e) = make_float4(db[v][e], db[v][e + 1], db[v][e + 2], db[v][e + 3]);
+        }
+      }
+  }
+}
+
 // Rows too wide for registers: one CTA a row at a time, swept from memory.
 template <typename T, bool BWD>
 __global__ void __launch_bounds__(kThreads) k_norm_wide(const Args a) {
-  __shared__ float2 red[2][kThreads / 32];
+  __shared__ float4 red[2][kMostThreads / 32];
   GroupSum<kThreads> sum{red};
   const int64_t cols = a.cols;
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * cols;
     const T* z = a.z ? static_cast<const T*>(a.z) + r * cols : nullptr;
-    float s = 0.f;
-    for (int64_t c = threadIdx.x; c < cols; c += kThreads) s += to_f(x[c]);
-    const float mean = sum(s, 0.f).x / (float)cols;
-    s = 0.f;
+    float s[1] = {0.f}, q[1] = {0.f};
+    for (int64_t c = threadIdx.x; c < cols; c += kThreads) s[0] += to_f(x[c]);
+    sum(s);
+    const float mean = s[0] / (float)cols;
     for (int64_t c = threadIdx.x; c < cols; c += kThreads) {
       const float d = to_f(x[c]) - mean;
-      s = fmaf(d, d, s);
+      q[0] = fmaf(d, d, q[0]);
     }
-    const float rstd = 1.f / sqrtf(sum(s, 0.f).x / (float)cols + a.eps);
+    sum(q);
+    const float rstd = 1.f / sqrtf(q[0] / (float)cols + a.eps);
     if constexpr (!BWD) {
       T* y = static_cast<T*>(a.out) + r * cols;
       for (int64_t c = threadIdx.x; c < cols; c += kThreads) {
@@ -300,7 +455,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_wide(const Args a) {
       }
     } else {
       const T* dout = static_cast<const T*>(a.dout) + r * cols;
-      float s1 = 0.f, s2 = 0.f;
+      float m[2] = {0.f, 0.f};
       for (int64_t c = threadIdx.x; c < cols; c += kThreads) {
         const float n = (to_f(x[c]) - mean) * rstd;
         float h = to_f(dout[c]);
@@ -311,11 +466,11 @@ __global__ void __launch_bounds__(kThreads) k_norm_wide(const Args a) {
               h * fmaf(n, w, a.b ? a.b[c] : 0.f) * (sg * fmaf(zv, 1.f - sg, 1.f)));
           h *= zv * sg;
         }
-        s1 += h * w;
-        s2 = fmaf(h * w, n, s2);
+        m[0] += h * w;
+        m[1] = fmaf(h * w, n, m[1]);
       }
-      const float2 m = sum(s1, s2);
-      const float m1 = m.x / (float)cols, m2 = m.y / (float)cols;
+      sum(m);
+      const float m1 = m[0] / (float)cols, m2 = m[1] / (float)cols;
       if (threadIdx.x == 0) a.stat[2 * r] = mean, a.stat[2 * r + 1] = rstd;
       T* dx = static_cast<T*>(a.out) + r * cols;
       for (int64_t c = threadIdx.x; c < cols; c += kThreads) {
@@ -372,40 +527,63 @@ __global__ void __launch_bounds__(kThreads) k_norm_sum(const float* __restrict__
   }
 }
 
-template <typename T, int E, int GT, int VPL, bool BWD>
-cudaError_t launch(const Args& a, cudaStream_t st, int* parts) {
-  constexpr int GC = kThreads / GT;
-  const int64_t need = (a.rows + GC - 1) / GC, most = BWD ? kParts : 8 * kSMs;
+// MINB CTAs an SM, which the kernel's registers allow, and one grid of them.
+// `threads`: of a CTA that takes one row; else GT threads take one.
+template <typename T, int E, int GT, int VPL, int BT, int MINB, bool BWD>
+cudaError_t launch(const Args& a, cudaStream_t st, int* parts, int threads = kThreads) {
+  constexpr int GC = GT > 32 ? 1 : kThreads / GT;
+  const int64_t need = (a.rows + GC - 1) / GC, most = MINB * kSMs;
+  static_assert(!BWD || MINB * kSMs <= kParts, "partial sums");
   const unsigned grid = (unsigned)(need < most ? need : most);
   *parts = (int)grid;
-  if (a.z) k_norm<T, E, GT, VPL, BWD, true><<<grid, kThreads, 0, st>>>(a);
-  else k_norm<T, E, GT, VPL, BWD, false><<<grid, kThreads, 0, st>>>(a);
+  if (a.z) k_norm<T, E, GT, VPL, BT, MINB, BWD, true><<<grid, threads, 0, st>>>(a);
+  else k_norm<T, E, GT, VPL, BT, MINB, BWD, false><<<grid, threads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+template <int VPL, int BT, int MINB, bool BWD>
+cudaError_t launch_row(const Args& a, cudaStream_t st, int* parts) {
+  const int64_t most = MINB * kSMs;
+  const unsigned grid = (unsigned)(a.rows < most ? a.rows : most);
+  *parts = (int)grid;
+  const int threads = (int)((a.cols / 8 + 32 * VPL - 1) / (32 * VPL) * 32);
+  const size_t smem = (size_t)a.cols * (BWD && !a.z ? 4 : 8);  // at most 64 KB
+  const auto kern = a.z ? k_norm_row<VPL, BT, MINB, BWD, true> : k_norm_row<VPL, BT, MINB, BWD, false>;
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<grid, threads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
-// The group and the packs of a thread by the row's packs: part of a warp up to
-// 128 packs (no barrier), else a CTA.
+// The group by the row's packs: part of a warp up to 64 packs (no barrier),
+// else a CTA of as many threads as the row needs with one or two packs each.
 template <typename T, bool BWD>
 cudaError_t launch_rows(const Args& a, bool vec, cudaStream_t st, int* parts, bool* wide) {
-  constexpr int E = 16 / (int)sizeof(T);
+  constexpr int E = 16 / (int)sizeof(T), kB = BWD ? 2 : 4;
   *wide = false;
+  const auto warps = [](int64_t n) { return (int)((n + 31) / 32 * 32); };
   if (vec) {
-    const int64_t n = (a.cols + E - 1) / E;
-    if (n <= 4) return launch<T, E, 4, 1, BWD>(a, st, parts);
-    if (n <= 8) return launch<T, E, 8, 1, BWD>(a, st, parts);
-    if (n <= 16) return launch<T, E, 16, 1, BWD>(a, st, parts);
-    if (n <= 32) return launch<T, E, 32, 1, BWD>(a, st, parts);
-    if (n <= 64) return launch<T, E, 32, 2, BWD>(a, st, parts);
-    if (n <= 256) return launch<T, E, 256, 1, BWD>(a, st, parts);
-    if (n <= 512) return launch<T, E, 256, 2, BWD>(a, st, parts);
-    if (n <= 768) return launch<T, E, 256, 3, BWD>(a, st, parts);
-    if (n <= 1024) return launch<T, E, 256, 4, BWD>(a, st, parts);
+    const int64_t n = a.cols / E;
+    if (n <= 4) return launch<T, E, 4, 1, 256, kB, BWD>(a, st, parts);
+    if (n <= 8) return launch<T, E, 8, 1, 256, kB, BWD>(a, st, parts);
+    if (n <= 16) return launch<T, E, 16, 1, 256, kB, BWD>(a, st, parts);
+    if (n <= 32) return launch<T, E, 32, 1, 256, kB, BWD>(a, st, parts);
+    if (n <= 64) return launch<T, E, 32, 2, 256, 2, BWD>(a, st, parts);
+    if constexpr (sizeof(T) == 2) {
+      if (n <= 256) return launch_row<1, 256, BWD ? 3 : 4, BWD>(a, st, parts);
+      if (n <= 640) return launch_row<2, 320, BWD ? 2 : 3, BWD>(a, st, parts);
+      if (n <= 1024) return launch_row<2, 512, 1, BWD>(a, st, parts);
+    } else {
+      if (n <= 256) return launch<T, E, 64, 1, 256, kB, BWD>(a, st, parts, warps(n));
+      if (n <= 1024) return launch<T, E, 64, 2, 512, 1, BWD>(a, st, parts, warps((n + 1) / 2));
+    }
   } else {
-    if (a.cols <= 8) return launch<T, 1, 8, 1, BWD>(a, st, parts);
-    if (a.cols <= 32) return launch<T, 1, 32, 1, BWD>(a, st, parts);
-    if (a.cols <= 160) return launch<T, 1, 32, 5, BWD>(a, st, parts);
-    if (a.cols <= 1024) return launch<T, 1, 256, 4, BWD>(a, st, parts);
-    if (a.cols <= 4096) return launch<T, 1, 256, 16, BWD>(a, st, parts);
+    if (a.cols <= 8) return launch<T, 1, 8, 1, 256, kB, BWD>(a, st, parts);
+    if (a.cols <= 32) return launch<T, 1, 32, 1, 256, kB, BWD>(a, st, parts);
+    if (a.cols <= 160) return launch<T, 1, 32, 5, 256, BWD ? 3 : 4, BWD>(a, st, parts);
+    if (a.cols <= 1024) return launch<T, 1, 64, 4, 256, kB, BWD>(a, st, parts, warps((a.cols + 3) / 4));
+    if (a.cols <= 4096) return launch<T, 1, 64, 8, 512, 1, BWD>(a, st, parts, warps((a.cols + 7) / 8));
   }
   *wide = true;
   const unsigned grid = (unsigned)(a.rows < 4 * kSMs ? a.rows : 4 * kSMs);

@@ -2,14 +2,14 @@
 // ssd_delta_bwd.cu): the run list, the warp-level matrix instruction, and the
 // operand split that keeps fp32 accuracy on 16-bit matrix instructions.
 //
-// Operands.  Every matrix operand is held as fp16 after its rows (for the
-// tiles of q, k and the inverse: the tile) have been brought to [2^14, 2^15) by a power of
-// two that is folded back into the fp32 result (pow2_scale).  A bf16 value is
-// then exact in one term (8 bits, down to 2^-28 of the largest); an fp32 one
-// is split in two, hi + lo with 11 bits each, so that a product of an exact
-// and a split operand takes two instructions and is off by about 2^-22, and
-// one of two split operands takes three (lo * lo is left out: 2^-22 again).
-// bf16 terms would need three and six for the same accuracy.
+// Operands.  Every matrix operand is held as fp16 after its rows (for q and k:
+// the chunk's tile) have been brought into fp16's range by a power of two that
+// is folded back into the fp32 result.  A bf16 value is then exact in one term
+// (8 bits, down to 2^-17 of the largest, and off by 2^-25 of it below); an
+// fp32 one is split in two, hi + lo with 11 bits each, so that a product of an
+// exact and a split operand takes two instructions and is off by about 2^-22,
+// and one of two split operands takes three (lo * lo is left out: 2^-22
+// again).  bf16 terms would need three and six for the same accuracy.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -70,6 +70,15 @@ __device__ __forceinline__ float pow2_scale(float m, float& inv) {
   return __uint_as_float((uint32_t)(268 - e) << 23);
 }
 
+// The same for tiles of q and k, brought to [1, 2): their products with a state
+// of up to 2^14 then stay in its units (ssd_delta_walk.cuh).
+__device__ __forceinline__ float pow2_unit(float m, float& inv) {
+  int e = (int)(__float_as_uint(m) >> 23);
+  e = e < 1 ? 1 : e > 253 ? 253 : e;
+  inv = __uint_as_float((uint32_t)e << 23);
+  return __uint_as_float((uint32_t)(254 - e) << 23);
+}
+
 __device__ __forceinline__ uint32_t pack2(float2 v) {
   const __half2 h = __float22half2_rn(v);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -93,7 +102,7 @@ __device__ __forceinline__ float2 mul2(float a, float b, float s) { return __fmu
 // as it stands, and a product can be fed to the next without leaving the
 // registers.
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));

@@ -17,8 +17,10 @@
 // accuracy (split operands), dk only to its type's.
 //
 // One CTA takes 64 tokens of a group, a slice of the columns n, and some of the
-// group's heads, whose dq and dk it adds in registers in a fixed order; eight
-// warps: four times 16 rows, two halves of the columns.
+// group's heads, whose dq and dk it adds in registers in a fixed order; sixteen
+// warps: four times 16 rows, four quarters of the columns.  (Eight warps with
+// twice the columns each took 1.4 times as long: between its barriers a warp's
+// instructions depend on one another, and two warps a scheduler do not fill it.)
 #pragma once
 
 #include "ssd_delta_prep.cuh"
@@ -26,7 +28,7 @@
 namespace ssd {
 namespace delta {
 
-constexpr int kGradThreads = 256;
+constexpr int kGradThreads = 512, kGradWarps = kGradThreads / 32;
 constexpr int kPS = 64;  // headdim columns staged at once
 
 struct GradArgs {
@@ -105,16 +107,15 @@ __device__ __forceinline__ void product(float (&acc)[TN][4], uint32_t a, int as,
     for (int t = 0; t < TA; ++t) a_frag<AW, ATRANS>(a + t * as, m0, 16 * k, lane, A[t]);
 #pragma unroll
     for (int t = 0; t < TB; ++t)
+      {
+        uint32_t B[TN / 2][4];
 #pragma unroll
-      for (int np = 0; np < TN / 2; np += 2) {
-        uint32_t B[2][4];
+        for (int x = 0; x < TN / 2; ++x) ldsm4t(b + t * bs + tile_off<BW>(16 * k + tr, n0 + 16 * x + nc), B[x]);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) ldsm4t(b + t * bs + tile_off<BW>(16 * k + tr, n0 + 16 * (np + x) + nc), B[x]);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) mma(acc[2 * np + x], A[0], B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
+        for (int x = 0; x < TN; ++x) mma(acc[x], A[0], B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
         if (TA == 2 && t == 0) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x) mma(acc[2 * np + x], A[TA - 1], B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
+          for (int x = 0; x < TN; ++x) mma(acc[x], A[TA - 1], B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
         }
       }
   }
@@ -179,15 +180,15 @@ template <typename T, int NT>
 __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs a) {
   using G = GradTiles<T, NT>;
   using X = TokenTiles<T, NT>;
-  constexpr int NS = G::kNS, TM = G::kTerms, TN = NS / 16;  // accumulator tiles of a warp: half the columns
+  constexpr int NS = G::kNS, TM = G::kTerms, TN = NS / 32;  // accumulator tiles of a warp: a quarter of the columns
   extern __shared__ __align__(128) char sm[];
   __shared__ double cs[kCheck];
   __shared__ __align__(16) float into[kCheck], outof[kCheck], inv[kCheck], bet[kCheck];
-  __shared__ float sums[3][kCheck];     // d.e, dv.v, and q.dq of the second half of the columns
-  __shared__ float wmax[3][8], wpi[8];
+  __shared__ float sums[6][kCheck];     // d.e, dv.v, and q.dq of each quarter of the columns
+  __shared__ float wmax[3][kGradWarps], wpi[kGradWarps], most[2][5];
   __shared__ int plain_s;
   const uint32_t smu = sm100::smem_u32(sm);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mt = warp & 3, half = warp >> 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mt = warp & 3, quarter = warp >> 2;
   int64_t u = blockIdx.x;
   const int split = (int)(u % a.splits);
   u /= a.splits;
@@ -248,76 +249,88 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
     const Factors* f1 = reinterpret_cast<const Factors*>(reinterpret_cast<const char*>(f) +
                                                          (nch == 2 ? a.H * HeadTiles<2>::kBytes : 0));
     const float ik[2] = {f->ik, f1->ik}, iq[2] = {f->iq, f1->iq};
-    float P[2][2][4], Z[2][2][4], dqh[TN][4];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) clear(P[b]), clear(Z[b]);
+    const int sb = quarter;  // this warp's block of P and Z: rows 16 mt.., columns 16 sb.., if not above the diagonal
+    float P[2][4], Z[2][4], dqh[TN][4];
+    clear(P);
+    clear(Z);
     clear(dqh);
     float pi = 0.f;
     for (int p0 = 0; p0 < a.P; p0 += kPS) {
-      // the scales: largest magnitudes the walks left, by 16 rows of the state
-      float my = 0.f, me = 0.f, md = 0.f, ms = 0.f, mds = 0.f;
-      for (int i = p0 / 16; i < a.pg && i < p0 / 16 + kPS / 16; ++i) {
-        for (int c = 0; c < nch; ++c) {
-          const int64_t o = ((int64_t)(sl.chunk + c) * a.H + h) * a.pg + i;
-          my = fmaxf(my, a.max_y[o]), me = fmaxf(me, a.max_e[o]), md = fmaxf(md, a.max_d[o]);
-        }
-        const int64_t o = (slot * a.H + h) * a.pg + i;
-        ms = fmaxf(ms, a.max_s[o]), mds = fmaxf(mds, a.max_ds[o]);
+      // the scales: largest magnitudes the walks left, by 16 rows of the
+      // state; a warp for each of the five
+      if (warp >= 1 && warp <= 5) {
+        const int i = p0 / 16 + (lane & 3), c = (lane >> 2) & 1;
+        const bool in = i < a.pg && (c == 0 || (warp <= 3 && nch == 2));
+        const float* src = warp == 1 ? a.max_y : warp == 2 ? a.max_e : warp == 3 ? a.max_d : warp == 4 ? a.max_s : a.max_ds;
+        const int64_t row = warp <= 3 ? (int64_t)(sl.chunk + c) * a.H + h : slot * a.H + h;
+        const float m = absmax_bits(in ? __float_as_uint(src[row * a.pg + i]) : 0u);
+        if (lane == 0) most[p0 / kPS & 1][warp - 1] = m;
       }
-      float iy, ie, id, is, ids;
-      const float sy = pow2_scale(my, iy), se = pow2_scale(me, ie), sd = pow2_scale(md, id), ss = pow2_scale(ms, is),
-                  sds = pow2_scale(mds, ids);
       __syncthreads();  // the factors are there; the previous slice's tiles are read
+      const float* mx = most[p0 / kPS & 1];
+      float iy, ie, id, is, ids;
+      const float sy = pow2_scale(mx[0], iy), se = pow2_scale(mx[1], ie), sd = pow2_scale(mx[2], id),
+                  ss = pow2_scale(mx[3], is), sds = pow2_scale(mx[4], ids);
       const bool v4 = a.P % 4 == 0;
+      {  // all loads before the first use
+        constexpr int kIt = 64 * 16 / kGradThreads, kRows = kGradThreads / 16;
+        float e4[kIt][4], d4[kIt][4], u4[kIt][4], y4[kIt][4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int t = (threadIdx.x >> 4) + 16 * x, p = (threadIdx.x & 15) * 4;
-        const int left = t < sl.n ? (int)(a.P - p0 - p) : 0;
-        const int64_t o = (((int64_t)sl.tok + t) * a.H + h) * a.P + p0 + p;
-        float e4[4], d4[4], v4v[4], y4[4];
-        get4(a.e + o, left, v4, e4);
-        get4(a.d + o, left, v4, d4);
-        get4(static_cast<const T*>(a.dy) + o, left, a.vec, y4);
-        get4(static_cast<const T*>(a.v) + o, left, a.vec, v4v);
-        float de = 0.f, dv = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) de = fmaf(d4[i], e4[i], de), dv = fmaf(d4[i], v4v[i], dv);
-#pragma unroll
-        for (int i = 8; i > 0; i >>= 1) {
-          de += __shfl_xor_sync(0xffffffffu, de, i);
-          dv += __shfl_xor_sync(0xffffffffu, dv, i);
+        for (int x = 0; x < kIt; ++x) {
+          const int t = (threadIdx.x >> 4) + kRows * x, p = (threadIdx.x & 15) * 4;
+          const int left = t < sl.n ? (int)(a.P - p0 - p) : 0;
+          const int64_t o = (((int64_t)sl.tok + t) * a.H + h) * a.P + p0 + p;
+          get4(a.e + o, left, v4, e4[x]);
+          get4(a.d + o, left, v4, d4[x]);
+          get4(static_cast<const T*>(a.dy) + o, left, a.vec, y4[x]);
+          get4(static_cast<const T*>(a.v) + o, left, a.vec, u4[x]);
         }
-        if ((lane & 15) == 0) sums[0][t] += de, sums[1][t] += dv;  // one thread of its own for each t
-        const uint32_t to = tile_off<64>(t, p);
-        put4<2>(sm + G::kE, G::kSmall, to, e4, se);
-        put4<TM>(sm + G::kD, G::kSmall, to, d4, sd);
-        put4<TM>(sm + G::kY, G::kSmall, to, y4, sy);
+#pragma unroll
+        for (int x = 0; x < kIt; ++x) {
+          const int t = (threadIdx.x >> 4) + kRows * x, p = (threadIdx.x & 15) * 4;
+          float de = 0.f, dv = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) de = fmaf(d4[x][i], e4[x][i], de), dv = fmaf(d4[x][i], u4[x][i], dv);
+#pragma unroll
+          for (int i = 8; i > 0; i >>= 1) {
+            de += __shfl_xor_sync(0xffffffffu, de, i);
+            dv += __shfl_xor_sync(0xffffffffu, dv, i);
+          }
+          if ((lane & 15) == 0) sums[0][t] += de, sums[1][t] += dv;  // one thread of its own for each t
+          const uint32_t to = tile_off<64>(t, p);
+          put4<2>(sm + G::kE, G::kSmall, to, e4[x], se);
+          put4<TM>(sm + G::kD, G::kSmall, to, d4[x], sd);
+          put4<TM>(sm + G::kY, G::kSmall, to, y4[x], sy);
+        }
       }
       const bool n4 = a.N % 4 == 0;
       const float* sc = sl.fin == kInside ? a.s + (slot + 1) * a.H * a.P * a.N
                         : a.s_fin && sl.fin >= 0 ? a.s_fin + (int64_t)sl.fin * a.H * a.P * a.N : nullptr;
-      for (int i = threadIdx.x; i < kPS * (NS / 4); i += kGradThreads) {
-        const int p = i / (NS / 4), n = (i % (NS / 4)) * 4;
-        const int left = p0 + p < a.P ? (int)(a.N - n0 - n) : 0;
-        const int64_t o = (h * a.P + p0 + p) * a.N + n0 + n, ol = slot * a.H * a.P * a.N + o;
-        float x[4], y[4], z[4];
-        get4(a.s + ol, left, n4, x);
-        get4(a.ds + ol, left, n4, y);
-        if (sc) {
-          get4(sc + o, left, n4, z);
+      {
+        constexpr int kIt = kPS * (NS / 4) / kGradThreads;
+        float x[kIt][4], y[kIt][4], z[kIt][4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) pi = fmaf(y[e], z[e], pi);
+        for (int i = 0; i < kIt; ++i) {
+          const int at = threadIdx.x + i * kGradThreads, p = at / (NS / 4), n = (at % (NS / 4)) * 4;
+          const int left = p0 + p < a.P ? (int)(a.N - n0 - n) : 0;
+          const int64_t o = (h * a.P + p0 + p) * a.N + n0 + n, ol = slot * a.H * a.P * a.N + o;
+          get4(a.s + ol, left, n4, x[i]);
+          get4(a.ds + ol, left, n4, y[i]);
+          get4(sc ? sc + o : a.s, sc ? left : 0, n4, z[i]);
         }
-        const uint32_t to = tile_off<NS>(p, n);
-        put4<2>(sm + G::kS, G::kTok, to, x, ss);
-        put4<TM>(sm + G::kDS, G::kTok, to, y, sds);
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+          const int at = threadIdx.x + i * kGradThreads, p = at / (NS / 4), n = (at % (NS / 4)) * 4;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pi = fmaf(y[i][e], z[i][e], pi);
+          const uint32_t to = tile_off<NS>(p, n);
+          put4<2>(sm + G::kS, G::kTok, to, x[i], ss);
+          put4<TM>(sm + G::kDS, G::kTok, to, y[i], sds);
+        }
       }
       __syncthreads();
       // dY E^T and D E^T, blocks of 16 tokens on and below the diagonal
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int sb = 2 * half + b;
-        if (sb > mt) continue;
+      if (sb <= mt) {
         float x[2][4], z[2][4];
         clear(x);
         clear(z);
@@ -338,17 +351,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
             mma(z[i], D[0], E[0][2 * i], E[0][2 * i + 1]);
             mma(x[i], Y[0], E[1][2 * i], E[1][2 * i + 1]);
             if constexpr (TM == 2) {
-              mma(x[i], Y[1], E[0][2 * i], E[0][2 * i + 1]);
+              mma(x[i], Y[TM - 1], E[0][2 * i], E[0][2 * i + 1]);
               mma(z[i], D[0], E[1][2 * i], E[1][2 * i + 1]);
-              mma(z[i], D[1], E[0][2 * i], E[0][2 * i + 1]);
+              mma(z[i], D[TM - 1], E[0][2 * i], E[0][2 * i + 1]);
             }
           }
         }
-        add_rows(P[b], x, iy * ie, iy * ie);
-        add_rows(Z[b], z, id * ie, id * ie);
+        add_rows(P, x, iy * ie, iy * ie);
+        add_rows(Z, z, id * ie, id * ie);
       }
       float tmp[TN][4];
-      const int nb = half * (NS / 2);
+      const int nb = quarter * (NS / 4);
       clear(tmp);
       product<TN, 64, false, TM, NS, 2>(tmp, smu + G::kY, G::kSmall, 16 * mt, smu + G::kS, G::kTok, nb, 0, kPS / 16, lane);
       add_rows(dqh, tmp, a.scale * into[r0] * (iy * is), a.scale * into[r0 + 8] * (iy * is));
@@ -362,10 +375,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
     // P and Z with their decays; the scales of the chunks' k and q go with the
     // token that is summed over
     float m1 = 0.f, m2 = 0.f, m3 = 0.f;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int sb = 2 * half + b;
-      if (sb > mt) continue;
+    if (sb <= mt) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -373,11 +383,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
           const int t = r0 + 8 * (e >> 1), s = 16 * sb + 8 * i + 2 * (lane & 3) + (e & 1);
           float w = 0.f;
           if (s <= t) w = (plain_s ? into[t] * inv[s] : pow2_of(cs[t] - cs[s])) * bet[s];
-          P[b][i][e] *= a.scale * w;
-          Z[b][i][e] *= s < t ? -bet[t] * w : 0.f;
-          m1 = fmaxf(m1, fabsf(P[b][i][e]) * ik[s >> 5]);
-          m2 = fmaxf(m2, fabsf(P[b][i][e]) * iq[t >> 5]);
-          m3 = fmaxf(m3, fabsf(Z[b][i][e]) * fmaxf(ik[t >> 5], ik[s >> 5]));
+          P[i][e] *= a.scale * w;
+          Z[i][e] *= s < t ? -bet[t] * w : 0.f;
+          m1 = fmaxf(m1, fabsf(P[i][e]) * ik[s >> 5]);
+          m2 = fmaxf(m2, fabsf(P[i][e]) * iq[t >> 5]);
+          m3 = fmaxf(m3, fabsf(Z[i][e]) * fmaxf(ik[t >> 5], ik[s >> 5]));
         }
     }
     m1 = absmax_bits(__float_as_uint(m1)), m2 = absmax_bits(__float_as_uint(m2)), m3 = absmax_bits(__float_as_uint(m3));
@@ -387,13 +397,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
     __syncthreads();
     m1 = m2 = m3 = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m1 = fmaxf(m1, wmax[0][i]), m2 = fmaxf(m2, wmax[1][i]), m3 = fmaxf(m3, wmax[2][i]);
+    for (int i = 0; i < kGradWarps; ++i) m1 = fmaxf(m1, wmax[0][i]), m2 = fmaxf(m2, wmax[1][i]), m3 = fmaxf(m3, wmax[2][i]);
     float i1, i2, i3;
     const float s1 = pow2_scale(m1, i1), s2 = pow2_scale(m2, i2), s3 = pow2_scale(m3, i3);
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int sb = 2 * half + b;
-      if (sb > mt) continue;
+    if (sb <= mt) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -401,7 +408,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
           const int t = r0 + 8 * hh, s = 16 * sb + 8 * i + 2 * (lane & 3);
           const uint32_t o = tile_off<64>(t, s);
           const float ks = ik[s >> 5], kt = ik[t >> 5], qt = iq[t >> 5];
-          const float pa = P[b][i][2 * hh], pb = P[b][i][2 * hh + 1], za = Z[b][i][2 * hh], zb = Z[b][i][2 * hh + 1];
+          const float pa = P[i][2 * hh], pb = P[i][2 * hh + 1], za = Z[i][2 * hh], zb = Z[i][2 * hh + 1];
           const auto put = [&](int at, bool two, float2 x) {
             uint32_t hi, lo;
             split2(x, hi, lo);
@@ -417,7 +424,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
     __syncthreads();
     {
       float tmp[TN][4];
-      const int nb = half * (NS / 2);
+      const int nb = quarter * (NS / 4);
       clear(tmp);
       product<TN, 64, false, 2, NS, TM>(tmp, smu + G::kW1, G::kSmall, 16 * mt, smu + G::kK, G::kTok, nb, 0, mt + 1, lane);
       add_rows(dqh, tmp, i1, i1);
@@ -449,13 +456,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
         q1 += __shfl_xor_sync(0xffffffffu, q1, o);
       }
       q0 *= iq[r0 >> 5], q1 *= iq[(r0 + 8) >> 5];
-      if (half == 1 && (lane & 3) == 0) sums[2][r0] = q0, sums[2][r0 + 8] = q1;
+      if ((lane & 3) == 0) sums[2 + quarter][r0] = q0, sums[2 + quarter][r0 + 8] = q1;
       __syncthreads();
-      if (half == 0 && (lane & 3) == 0) {
-        float* o = a.qdq + (int64_t)ns * a.part_stride + ((int64_t)sl.tok + r0) * a.H + h;
-        if (r0 < sl.n) o[0] = q0 + sums[2][r0];
-        if (r0 + 8 < sl.n) o[8 * a.H] = q1 + sums[2][r0 + 8];
-      }
+      if (threadIdx.x < sl.n)
+        a.qdq[(int64_t)ns * a.part_stride + ((int64_t)sl.tok + threadIdx.x) * a.H + h] =
+            (sums[2][threadIdx.x] + sums[3][threadIdx.x]) + (sums[4][threadIdx.x] + sums[5][threadIdx.x]);
       add_rows(dq, dqh, 1.f, 1.f);
     }
     if (ns == 0 && threadIdx.x < sl.n) {
@@ -466,7 +471,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
     if (threadIdx.x == 0) {
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += wpi[i];
+      for (int i = 0; i < kGradWarps; ++i) s += wpi[i];
       a.pi[((int64_t)ns * a.slots_n + slot) * a.H + h] = s;
     }
   }
@@ -477,7 +482,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
     for (int i = 0; i < TN; ++i)
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
-        const int t = r0 + 8 * hh, n = n0 + half * (NS / 2) + 8 * i + 2 * (lane & 3);
+        const int t = r0 + 8 * hh, n = n0 + quarter * (NS / 4) + 8 * i + 2 * (lane & 3);
         if (t >= sl.n || n >= a.N) continue;
         const float x = (w ? dk : dq)[i][2 * hh], y = (w ? dk : dq)[i][2 * hh + 1];
         const int64_t o = (((int64_t)sl.tok + t) * a.G + grp) * a.N + n;

@@ -38,12 +38,14 @@ struct alignas(16) Factors {
   float kc[kC];   // forward: exp(cs) / k scale;  reverse: exp(cs_C - cs) / k scale
   float qc[kC];   // scale exp(cs) / q scale
   float uc[kC];   // forward: exp(cs_C - cs) beta / k scale;  reverse: -beta exp(cs) / k scale
-  float tau[kC];  // 1 / scale of the rows of the inverse
+  float tau[kC];  // 1 / scale of the rows of the inverse (forward: times 1 / norm)
   float mu[kC];   // 1 / scale of the rows of M
   float beta[kC];
-  float whole;    // exp(cs_C)
-  float ik, iq;   // 1 / scale of the chunk's k and q tiles
-  float pad;
+  float whole;     // exp(cs_C)
+  float ik, iq;    // 1 / scale of the chunk's k and q tiles
+  float norm;      // forward: a power of two that no row sum of the inverse's magnitudes exceeds
+  float ucm, qcm;  // largest magnitudes of uc and qc
+  float pad[2];
 };
 
 // Sizes of the images, in bytes.
@@ -179,8 +181,8 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(const PrepArgs a) {
     }
     __syncthreads();
     float sc[2];
-    sc[0] = pow2_scale(fmaxf(fmaxf(maxes[0][0], maxes[0][1]), fmaxf(maxes[0][2], maxes[0][3])), inv_k);
-    sc[1] = pow2_scale(fmaxf(fmaxf(maxes[1][0], maxes[1][1]), fmaxf(maxes[1][2], maxes[1][3])), inv_q);
+    sc[0] = pow2_unit(fmaxf(fmaxf(maxes[0][0], maxes[0][1]), fmaxf(maxes[0][2], maxes[0][3])), inv_k);
+    sc[1] = pow2_unit(fmaxf(fmaxf(maxes[1][0], maxes[1][1]), fmaxf(maxes[1][2], maxes[1][3])), inv_q);
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
@@ -315,16 +317,28 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(const PrepArgs a) {
         }
         t[s] = (s == lane ? 1.f : 0.f) - ((p[0] + p[1]) + (p[2] + p[3]));
       }
-      f->tau[lane] = store_row(t, lane, img, img + kSq);
+      float tau = store_row(t, lane, img, img + kSq);
+      const float uc = (rev ? -into : outof) * bt * inv_k, qc = a.scale * into * inv_q;
+      const float ucm = absmax_bits(__float_as_uint(fabsf(uc))), qcm = absmax_bits(__float_as_uint(fabsf(qc)));
+      float norm = 1.f;
+      if (!rev) {
+        float l1 = 0.f;
+#pragma unroll
+        for (int s = 0; s < kC; ++s) l1 += fabsf(t[s]);
+        const uint32_t e = __float_as_uint(absmax_bits(__float_as_uint(l1))) >> 23;  // at least 127: the diagonal is 1
+        norm = __uint_as_float((e < 252 ? e + 1 : 253) << 23);
+        tau *= __uint_as_float((e < 252 ? 253 - e : 1) << 23);
+      }
+      f->tau[lane] = tau;
       f->kc[lane] = (rev ? outof : into) * inv_k;
-      f->uc[lane] = (rev ? -into : outof) * bt * inv_k;
+      f->uc[lane] = uc;
       f->beta[lane] = bt;
-      if (lane == 31) f->whole = into, f->ik = inv_k, f->iq = inv_q;
+      if (lane == 31) f->whole = into, f->ik = inv_k, f->iq = inv_q, f->norm = norm, f->ucm = ucm, f->qcm = qcm;
       if (rev || kFwdM) {
         row(gq, a.scale, 0, [&](int cidx, float w) { t[cidx] = w; });
         char* mi = img + (rev ? HR::kM : HF::kM);
         f->mu[lane] = store_row(t, lane, mi, (rev ? 2 : MT) == 2 ? mi + kSq : nullptr);
-        f->qc[lane] = a.scale * into * inv_q;
+        f->qc[lane] = qc;
       }
     }
   }

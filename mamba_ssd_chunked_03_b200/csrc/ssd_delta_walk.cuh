@@ -9,6 +9,16 @@
 // S' (A = U).  The warps share only the chunk's tiles, copied one chunk ahead
 // into the other of two buffers; one barrier a chunk is all the
 // synchronisation there is.
+//
+// Units.  A row of the state is S times a power of two, sig, with |S| <= bnd
+// <= 2^15: S is an fp16 operand as it stands (hi + lo).  A chunk decays S and
+// moves it to the units in which the bound of what comes out, bnd exp(cs_C) +
+// 64 max|U| (32 tokens, k below 2), lies in [2^14, 2^15); U is brought to the
+// same units and the products are added to S in place.  The bound is some
+// 2^10 above the values, which leaves them 2^4 or so, 2^29 above fp16's last
+// place; every eighth chunk it starts anew from the true maximum, so that it
+// does not run away where nothing decays.  Taking the maximum in every chunk
+// was measured too: 130 clocks a chunk and warp of 2970.
 #pragma once
 
 #include "ssd_delta_prep.cuh"
@@ -246,18 +256,94 @@ __device__ __forceinline__ void zero(float (&x)[4][4]) {
     for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
 }
 
-// Row scales that bring the state to fp16 range: the scale, and 1 / scale.
+// Row maxima of the state.
 template <int NT>
-__device__ __forceinline__ void state_max(const float (&S)[NT / 8][4], float& m0, float& m1) {
-  m0 = m1 = 0.f;
+__device__ __forceinline__ float2 state_max(const float (&S)[NT / 8][4]) {
+  float m0 = 0.f, m1 = 0.f;
 #pragma unroll
   for (int i = 0; i < NT / 8; ++i) {
     m0 = fmaxf(m0, fmaxf(fabsf(S[i][0]), fabsf(S[i][1])));
     m1 = fmaxf(m1, fmaxf(fabsf(S[i][2]), fabsf(S[i][3])));
   }
-  m0 = quad_max(m0), m1 = quad_max(m1);
+  return make_float2(quad_max(m0), quad_max(m1));
+}
+template <int NT>
+__device__ __forceinline__ void state_scale(float (&S)[NT / 8][4], float2 f) {
+#pragma unroll
+  for (int i = 0; i < NT / 8; ++i) {
+    const float2 x = mul2(S[i][0], S[i][1], f.x), y = mul2(S[i][2], S[i][3], f.y);
+    S[i][0] = x.x, S[i][1] = x.y, S[i][2] = y.x, S[i][3] = y.y;
+  }
 }
 
+// The units of a thread's two rows of the state.
+struct Unit {
+  float2 sig, bnd;
+
+  // The power of two that brings a bound to [2^14, 2^15) (zero: 1), and its inverse.
+  static __device__ __forceinline__ float of(float b, float& inv) {
+    int e = (int)(__float_as_uint(b) >> 23);
+    e = e < 15 ? 15 : e > 253 ? 253 : e;
+    e = b > 0.f ? e : 141;
+    inv = __uint_as_float((uint32_t)(268 - e) << 23);
+    return __uint_as_float((uint32_t)(e - 14) << 23);
+  }
+  // A state as it was loaded: true values.
+  template <int NT>
+  __device__ __forceinline__ void init(float (&S)[NT / 8][4]) {
+    const float2 m = state_max<NT>(S);
+    float2 inv;
+    sig = make_float2(of(m.x, inv.x), of(m.y, inv.y));
+    bnd = make_float2(m.x * inv.x, m.y * inv.y);
+    state_scale<NT>(S, inv);
+  }
+  // Decay the state by `whole` and bring it to units that also hold 32 tokens'
+  // addends of at most `add` (times k, below 2).  Returns 1 / sig.
+  template <int NT>
+  __device__ __forceinline__ float2 step(float (&S)[NT / 8][4], float whole, float2 add, bool look) {
+    if (look) bnd = state_max<NT>(S);
+    const float2 want = make_float2(sig.x * whole, sig.y * whole);
+    const float2 b = make_float2(fmaf(bnd.x, want.x, 64.f * add.x), fmaf(bnd.y, want.y, 64.f * add.y));
+    float2 inv;
+    sig = make_float2(of(b.x, inv.x), of(b.y, inv.y));
+    bnd = make_float2(b.x * inv.x, b.y * inv.y);
+    state_scale<NT>(S, make_float2(want.x * inv.x, want.y * inv.y));
+    return inv;
+  }
+};
+
+// x (p x t) times row and column factors: f.x, f.y for the two rows, c for the columns.
+__device__ __forceinline__ void scale_tile(float (&x)[4][4], const float* c, float2 f, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = *reinterpret_cast<const float2*>(c + 8 * i + 2 * (lane & 3));
+    const float2 a = __fmul2_rn(make_float2(x[i][0], x[i][1]), mul2(v.x, v.y, f.x));
+    const float2 b = __fmul2_rn(make_float2(x[i][2], x[i][3]), mul2(v.x, v.y, f.y));
+    x[i][0] = a.x, x[i][1] = a.y, x[i][2] = b.x, x[i][3] = b.y;
+  }
+}
+// to = x c f + to
+__device__ __forceinline__ void add_scaled(float (&to)[4][4], const float (&x)[4][4], const float* c, float2 f, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = *reinterpret_cast<const float2*>(c + 8 * i + 2 * (lane & 3));
+    const float2 a = __ffma2_rn(make_float2(x[i][0], x[i][1]), mul2(v.x, v.y, f.x), make_float2(to[i][0], to[i][1]));
+    const float2 b = __ffma2_rn(make_float2(x[i][2], x[i][3]), mul2(v.x, v.y, f.y), make_float2(to[i][2], to[i][3]));
+    to[i][0] = a.x, to[i][1] = a.y, to[i][2] = b.x, to[i][3] = b.y;
+  }
+}
+// A tile whose values fit fp16 as they are, as operand tiles.
+template <bool LO>
+__device__ __forceinline__ void as_operand(const float (&x)[4][4], uint32_t (&hi)[2][4], uint32_t (&lo)[2][4]) {
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const float2 u = make_float2(x[2 * ks + (a >> 1)][2 * (a & 1)], x[2 * ks + (a >> 1)][2 * (a & 1) + 1]);
+      if constexpr (LO) split2(u, hi[ks][a], lo[ks][a]);
+      else hi[ks][a] = pack2(u);
+    }
+}
 // S += Uhi/lo (p x t) times a 32 x NT tile of tokens (k or q; TERMS fp16
 // terms).  Four tiles at a time, so that an accumulator is not needed again
 // before its last product is done.
@@ -303,6 +389,23 @@ __device__ __forceinline__ void tokens_mma(float (&d)[4][4], const uint32_t (&hi
 #pragma unroll
       for (int x = 0; x < 4; ++x) mma(d[x], lo, B[x >> 1][2 * (x & 1)], B[x >> 1][2 * (x & 1) + 1]);
     }
+  }
+}
+
+// acc (p x t) = S (in its units) times the rows of a tile of tokens; Y: and y of another tile.
+template <int NT, int TERMS, bool Y>
+__device__ __forceinline__ void state_times(const float (&S)[NT / 8][4], float (&acc)[4][4], uint32_t kt, float (&y)[4][4],
+                                            uint32_t qt, int lane) {
+  zero(acc);
+  if constexpr (Y) zero(y);
+#pragma unroll
+  for (int ks = 0; ks < NT / 16; ++ks) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      split2(make_float2(S[2 * ks + (x >> 1)][2 * (x & 1)], S[2 * ks + (x >> 1)][2 * (x & 1) + 1]), hi[x], lo[x]);
+    tokens_mma<NT, TERMS, true>(acc, hi, lo, kt, ks, lane);
+    if constexpr (Y) tokens_mma<NT, TERMS, TERMS == 2>(y, hi, lo, qt, ks, lane);
   }
 }
 
@@ -371,7 +474,6 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(cons
   const char* head = a.heads + (run.chunk * a.H + h) * Hd::kBytes;
   const T* v = static_cast<const T*>(a.v) + (run.tok * a.H + h) * a.P + p_cta;
   float S[NT / 8][4];
-  float sig0 = 1.f, sig1 = 1.f;  // the state's rows are S times these
   if (a.s0 && run.h0 >= 0) {
     load_state<NT>(S, a.s0 + (((int64_t)run.h0 * a.H + h) * a.P + p0) * a.N, a.N, rows, lane);
   } else {
@@ -380,6 +482,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(cons
 #pragma unroll
       for (int e = 0; e < 4; ++e) S[i][e] = 0.f;
   }
+  Unit unit;
+  unit.init<NT>(S);
   char* stage = sm + B::kStage + warp * (kC * 20 * 4);
   sm100::griddep_wait();  // the tiles
   const auto fetch = [&](int j) {
@@ -397,105 +501,51 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(cons
     const Factors& f = *reinterpret_cast<const Factors*>(buf + B::kHead + Hd::kF);
     const uint32_t kt = sm100::smem_u32(buf), qt = kt + kTerms * X::kTile;
     const uint32_t tt = kt + B::kHead, mt = tt + Hd::kM;
-    float m0, m1, inv0, inv1;
-    state_max<NT>(S, m0, m1);
     if constexpr (MODE == kStates) {
       if ((j & 1) == 0) {
         const int64_t at = (run.slot + (j >> 1)) * a.H + h;
-        store_state<NT>(S, sig0, sig1, a.check + (at * a.P + p0) * a.N, a.N, rows, lane);
-        const float m = warp_absmax(fmaxf(m0 * sig0, m1 * sig1));
+        store_state<NT>(S, unit.sig.x, unit.sig.y, a.check + (at * a.P + p0) * a.N, a.N, rows, lane);
+        const float m = warp_absmax(fmaxf(unit.bnd.x * unit.sig.x, unit.bnd.y * unit.sig.y));
         if (lane == 0) a.max_check[at * a.pg + p0 / 16] = m;
       }
     }
-    const float sc0 = pow2_scale(m0, inv0), sc1 = pow2_scale(m1, inv1);
-    inv0 *= sig0, inv1 *= sig1;
-    float acc[4][4], yq[4][4];
-    zero(acc);
-    zero(yq);
-#pragma unroll
-    for (int ks = 0; ks < NT / 16; ++ks) {
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        split2(mul2(S[2 * ks + (x >> 1)][2 * (x & 1)], S[2 * ks + (x >> 1)][2 * (x & 1) + 1], x & 1 ? sc1 : sc0), hi[x], lo[x]);
-      tokens_mma<NT, kTerms, true>(acc, hi, lo, kt, ks, lane);
-      if constexpr (kY) tokens_mma<NT, kTerms, kTerms == 2>(yq, hi, lo, qt, ks, lane);
-    }
-    const int tc = 2 * (lane & 3);
+    float acc[4][4], y[4][4], e[4][4];
+    state_times<NT, kTerms, kY>(S, acc, kt, y, qt, lane);
     uint32_t hi[2][4], lo[2][4];
-    float e[4][4];
-    float2 iv;
-    {  // R = V - exp(cs) K S^T
-      float v[4][4];
-      load_v<T, B::kVP>(v, buf + B::kV, 16 * warp, lane);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 kc = *reinterpret_cast<const float2*>(f.kc + 8 * i + tc);
-        v[i][0] = fmaf(-(acc[i][0] * inv0), kc.x, v[i][0]);
-        v[i][1] = fmaf(-(acc[i][1] * inv0), kc.y, v[i][1]);
-        v[i][2] = fmaf(-(acc[i][2] * inv1), kc.x, v[i][2]);
-        v[i][3] = fmaf(-(acc[i][3] * inv1), kc.y, v[i][3]);
-      }
-      iv = to_operand<true>(v, hi, lo);
-    }
-    zero(e);  // E = R (I + A)^-T
+    // R = V - exp(cs) K S^T
+    load_v<T, B::kVP>(e, buf + B::kV, 16 * warp, lane);
+    add_scaled(e, acc, f.kc, make_float2(-unit.sig.x, -unit.sig.y), lane);
+    float2 iv = to_operand<true>(e, hi, lo);
+    // E = R (I + A)^-T, in units (1 / iv below) in which it is below 2^15 like R
+    zero(e);
     lower_mma<true, 2>(e, hi, lo, tt, lane);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 tau = *reinterpret_cast<const float2*>(f.tau + 8 * i + tc);
-      e[i][0] *= iv.x * tau.x, e[i][1] *= iv.x * tau.y, e[i][2] *= iv.y * tau.x, e[i][3] *= iv.y * tau.y;
-    }
+    scale_tile(e, f.tau, make_float2(1.f, 1.f), lane);
+    iv.x *= f.norm, iv.y *= f.norm;
     const int n = run.len - j * kC < kC ? run.len - j * kC : kC;
     const int64_t row0 = ((run.tok + (int64_t)j * kC) * a.H + h) * a.P + p0;
     if constexpr (kY) {
-      iv = to_operand<kTerms == 2>(e, hi, lo);
+      as_operand<kTerms == 2>(e, hi, lo);
+      scale_tile(y, f.qc, unit.sig, lane);
       zero(acc);
       lower_mma<kTerms == 2, kMTerms>(acc, hi, lo, mt, lane);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 qc = *reinterpret_cast<const float2*>(f.qc + 8 * i + tc);
-        const float2 mu = *reinterpret_cast<const float2*>(f.mu + 8 * i + tc);
-        yq[i][0] = fmaf(yq[i][0] * inv0, qc.x, acc[i][0] * iv.x * mu.x);
-        yq[i][1] = fmaf(yq[i][1] * inv0, qc.y, acc[i][1] * iv.x * mu.y);
-        yq[i][2] = fmaf(yq[i][2] * inv1, qc.x, acc[i][2] * iv.y * mu.x);
-        yq[i][3] = fmaf(yq[i][3] * inv1, qc.y, acc[i][3] * iv.y * mu.y);
-      }
-      store_tile<T>(yq, stage, static_cast<T*>(a.out) + row0, a.H * a.P, n, rows, a.out_vec, lane);
+      add_scaled(y, acc, f.mu, iv, lane);
+      store_tile<T>(y, stage, static_cast<T*>(a.out) + row0, a.H * a.P, n, rows, a.out_vec, lane);
     } else {
-      store_tile<float>(e, stage, static_cast<float*>(a.out) + row0, a.H * a.P, n, rows, a.out_vec, lane);
-      const float m = warp_absmax(tile_max(e));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i][0] = e[i][0] * iv.x, y[i][1] = e[i][1] * iv.x, y[i][2] = e[i][2] * iv.y, y[i][3] = e[i][3] * iv.y;
+      store_tile<float>(y, stage, static_cast<float*>(a.out) + row0, a.H * a.P, n, rows, a.out_vec, lane);
+      const float m = warp_absmax(32768.f * fmaxf(iv.x, iv.y));
       if (lane == 0) a.max_out[((run.chunk + j) * a.H + h) * a.pg + p0 / 16] = m;
     }
-    // S' = exp(cs_C) S + U K, in units in which U fills fp16's range and S stays below 2^35
-    float u0 = 0.f, u1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 uc = *reinterpret_cast<const float2*>(f.uc + 8 * i + tc);
-      e[i][0] *= uc.x, e[i][1] *= uc.y, e[i][2] *= uc.x, e[i][3] *= uc.y;
-      u0 = fmaxf(u0, fmaxf(fabsf(e[i][0]), fabsf(e[i][1])));
-      u1 = fmaxf(u1, fmaxf(fabsf(e[i][2]), fabsf(e[i][3])));
-    }
-    u0 = fmaxf(quad_max(u0), m0 * sig0 * 0x1p-20f), u1 = fmaxf(quad_max(u1), m1 * sig1 * 0x1p-20f);
-    float n0, n1;
-    const float su0 = pow2_scale(u0, n0), su1 = pow2_scale(u1, n1);
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float s = x & 1 ? su1 : su0;
-        split2(mul2(e[2 * ks + (x >> 1)][2 * (x & 1)], e[2 * ks + (x >> 1)][2 * (x & 1) + 1], s), hi[ks][x], lo[ks][x]);
-      }
-    const float w0 = f.whole * sig0 * su0, w1 = f.whole * sig1 * su1;
-#pragma unroll
-    for (int i = 0; i < NT / 8; ++i) {
-      const float2 x = mul2(S[i][0], S[i][1], w0), y = mul2(S[i][2], S[i][3], w1);
-      S[i][0] = x.x, S[i][1] = x.y, S[i][2] = y.x, S[i][3] = y.y;
-    }
-    sig0 = n0, sig1 = n1;
+    // S' = exp(cs_C) S + U K
+    const float ub = 32768.f * f.ucm;
+    const float2 is = unit.step<NT>(S, f.whole, make_float2(iv.x * ub, iv.y * ub), (j & 7) == 7);
+    scale_tile(e, f.uc, make_float2(iv.x * is.x, iv.y * is.y), lane);
+    as_operand<true>(e, hi, lo);
     state_add<NT, kTerms>(S, hi, lo, kt, lane);
   }
   if (a.fin && run.fin >= 0)
-    store_state<NT>(S, sig0, sig1, a.fin + (((int64_t)run.fin * a.H + h) * a.P + p0) * a.N, a.N, rows, lane);
+    store_state<NT>(S, unit.sig.x, unit.sig.y, a.fin + (((int64_t)run.fin * a.H + h) * a.P + p0) * a.N, a.N, rows, lane);
 }
 
 // Launch a walk; its CTAs may start while the tiles' kernel ends.

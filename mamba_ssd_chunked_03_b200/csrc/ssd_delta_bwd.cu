@@ -36,8 +36,8 @@ Layout layout(const Shape& s, bool dfinal) {
   l.heads = (int)((hpg + splits - 1) / splits);
   l.splits = (int)((hpg + l.heads - 1) / l.heads);
   l.tokens = take(token_tiles_bytes(s));
-  l.fwd = take((size_t)s.chunks * s.H * HeadTiles<0>::kBytes);
-  l.rev = take((size_t)s.chunks * s.H * HeadTiles<2>::kBytes);
+  l.fwd = take((size_t)s.chunks * s.H * HeadTiles<0>::kStride);
+  l.rev = take((size_t)s.chunks * s.H * RevTiles::kStride);
   l.e = take(tokens * s.H * s.P * 4);
   l.d = take(tokens * s.H * s.P * 4);
   l.s = take((size_t)s.slots * hpn * 4);
@@ -84,7 +84,6 @@ cudaError_t run_all(const ssd_delta_bwd_args* b, const Shape& s, const Layout& l
   g.per_row = (int)((s.L + kCheck - 1) / kCheck), g.splits = l.splits, g.heads = l.heads, g.nslices = l.nslices;
   g.pg = l.pg, g.scale = s.scale, g.tokens = p.tokens, g.head = p.rev, g.v = a->v, g.dy = b->dy;
   g.e = at(l.e), g.d = at(l.d), g.s = at(l.s), g.ds = at(l.ds), g.s_fin = b->dfinal_states ? at(l.s_fin) : nullptr;
-  g.g = a->g, g.beta = a->beta;
   g.max_y = at(l.max_y), g.max_e = at(l.max_e), g.max_d = at(l.max_d), g.max_s = at(l.max_s), g.max_ds = at(l.max_ds);
   g.initial = a->initial_states != nullptr;
   g.slots = runs.slots, g.slots_n = s.slots, g.dq = b->dq, g.dk = b->dk;

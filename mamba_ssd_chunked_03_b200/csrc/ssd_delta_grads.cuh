@@ -19,7 +19,7 @@
 // One CTA takes 64 tokens of a group, a slice of the columns n, and some of the
 // group's heads, whose dq and dk it adds in registers in a fixed order; sixteen
 // warps: four times 16 rows, four quarters of the columns.  (Eight warps with
-// twice the columns each took 1.4 times as long: between its barriers a warp's
+// twice the columns each took 1.24 times as long: between its barriers a warp's
 // instructions depend on one another, and two warps a scheduler do not fill it.)
 #pragma once
 
@@ -39,7 +39,7 @@ struct GradArgs {
   int pg;
   float scale;
   const char* tokens;  // TokenTiles of both 32-token chunks
-  const char* head;    // HeadTiles<2> of the reverse walk: factors
+  const char* head;    // RevTiles: factors and decays
   const void* v;
   const void* dy;
   const float* e;
@@ -47,8 +47,6 @@ struct GradArgs {
   const float* s;       // [slot][head][P][N] states that enter
   const float* ds;      // gradients of the states that leave
   const float* s_fin;   // [run][head][P][N] last states, or null (no gradient comes in there)
-  const float* g;
-  const float* beta;
   const float *max_y, *max_e, *max_d, *max_s, *max_ds;
   const Slot* slots;    // packed, or null
   void* dq;
@@ -82,7 +80,13 @@ struct GradTiles {
   static constexpr int kW2 = kW1 + 2 * kSmall;         // P with q's scales, terms
   static constexpr int kZa = kW2 + kTerms * kSmall;    // Z with k's scales by row
   static constexpr int kZb = kZa + kTerms * kSmall;    // Z with k's scales by column
-  static constexpr int kBytes = kZb + kTerms * kSmall;
+  // E, D, V and dY of the next piece as they are in memory
+  static constexpr int kRawE = kZb + kTerms * kSmall, kRawD = kRawE + 64 * 64 * 4;
+  static constexpr int kRawV = kRawD + 64 * 64 * 4, kRawY = kRawV + 64 * 64 * (int)sizeof(T);
+  static constexpr int kRawEnd = kRawY + 64 * 64 * (int)sizeof(T);
+  // two terms of everything leave no room for them: they are read when needed
+  static constexpr bool kAhead = sizeof(T) == 2;
+  static constexpr int kBytes = kAhead ? kRawEnd : kRawE;
 };
 
 // A operand: rows row0.., columns col0.. of a row-major tile W wide; or, TRANS,
@@ -176,17 +180,46 @@ __device__ __forceinline__ Slot row_slot(const GradArgs& a, int64_t slot) {
   return s;
 }
 
+// Copy four elements, zeros where there are none: on their way if they lie on
+// a boundary of four (`vec`), at once otherwise.
+template <typename T>
+__device__ __forceinline__ void copy4(char* to, const T* base, int64_t o, int left, bool vec) {
+  if (vec) {
+    const T* p = left > 0 ? base + o : base;
+    if constexpr (sizeof(T) == 4) cp_async16(sm100::smem_u32(to), p, left > 0);
+    else cp_async8(sm100::smem_u32(to), p, left > 0);
+  } else {
+    T* d = reinterpret_cast<T*>(to);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = e < left ? base[o + e] : from_f<T>(0.f);
+  }
+}
+// four elements of shared memory
+__device__ __forceinline__ void get4(const float* p, float (&x)[4]) {
+  const float4 u = *reinterpret_cast<const float4*>(p);
+  x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+}
+__device__ __forceinline__ void get4(const __nv_bfloat16* p, float (&x)[4]) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  const float2 a = bf16x2(u.x), b = bf16x2(u.y);
+  x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+}
+
 template <typename T, int NT>
 __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs a) {
   using G = GradTiles<T, NT>;
   using X = TokenTiles<T, NT>;
   constexpr int NS = G::kNS, TM = G::kTerms, TN = NS / 32;  // accumulator tiles of a warp: a quarter of the columns
   extern __shared__ __align__(128) char sm[];
-  __shared__ double cs[kCheck];
-  __shared__ __align__(16) float into[kCheck], outof[kCheck], inv[kCheck], bet[kCheck];
-  __shared__ float sums[6][kCheck];     // d.e, dv.v, and q.dq of each quarter of the columns
-  __shared__ float wmax[3][kGradWarps], wpi[kGradWarps], most[2][5];
-  __shared__ int plain_s;
+  // of the 64 tokens: exp(cs), exp(cs_C - cs), 1 / exp(cs) within their 32-token
+  // chunk, and beta, as they were copied; exp(cs) and exp(cs_C - cs) over all 64
+  __shared__ __align__(16) float intol[kCheck], outl[kCheck], inv[kCheck], bet[kCheck], into[kCheck], outof[kCheck];
+  __shared__ __align__(16) float most[5][8];  // largest magnitudes: chunk (2), 16 columns of headdim (4)
+  __shared__ float whole[2];
+  __shared__ int plain[2];
+  __shared__ float scale[5], iscale[5];       // of Y, E, D, S, dS
+  __shared__ float sums[6][kCheck];           // d.e, dv.v, and q.dq of each quarter of the columns
+  __shared__ float wmax[3][kGradWarps], wpi[kGradWarps];
   const uint32_t smu = sm100::smem_u32(sm);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mt = warp & 3, quarter = warp >> 2;
   int64_t u = blockIdx.x;
@@ -198,6 +231,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
   const Slot sl = a.slots ? a.slots[slot] : row_slot(a, slot);
   if (sl.n == 0) return;
   const int nch = sl.n > kC ? 2 : 1, n0 = ns * NS;
+  const int64_t h0 = grp * a.hpg + (int64_t)split * a.heads;
+  const int64_t h1 = grp * a.hpg + ((int64_t)(split + 1) * a.heads < a.hpg ? (int64_t)(split + 1) * a.heads : a.hpg);
+  const auto image = [&](int c, int64_t h) { return a.head + ((int64_t)(sl.chunk + c) * a.H + h) * RevTiles::kStride; };
+  const auto decays = [&](int c, int64_t h) { return reinterpret_cast<const Decays*>(image(c, h) + RevTiles::kBytes); };
+  const auto factors = [&](int c, int64_t h) { return reinterpret_cast<const Factors*>(image(c, h) + RevTiles::kF); };
   // the group's k and q: this slice of both chunks' images
 #pragma unroll
   for (int w = 0; w < 2; ++w)
@@ -209,126 +247,172 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
       *reinterpret_cast<uint4*>(sm + dst) =
           r < kC * nch ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
     }
+  // 1 / scale of the chunks' k and q
+  const float ik0 = factors(0, h0)->ik, iq0 = factors(0, h0)->iq;
+  const float ik1 = nch == 2 ? factors(1, h0)->ik : ik0, iq1 = nch == 2 ? factors(1, h0)->iq : iq0;
   float dq[TN][4], dk[TN][4];
   clear(dq);
   clear(dk);
   const int r0 = 16 * mt + (lane >> 2);  // this thread's rows: r0, r0 + 8
-  const int64_t h1 = grp * a.hpg + ((int64_t)(split + 1) * a.heads < a.hpg ? (int64_t)(split + 1) * a.heads : a.hpg);
-  for (int64_t h = grp * a.hpg + (int64_t)split * a.heads; h < h1; ++h) {
-    __syncthreads();  // the previous head's tiles are read
-    if (warp == 0) {  // the 64 tokens' decays
-      double c2[2];
-      float b2[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = 2 * lane + i;
-        const int64_t o = ((int64_t)sl.tok + t) * a.H + h;
-        c2[i] = decay_log2(t < sl.n ? a.g[o] : 0.f);
-        b2[i] = t < sl.n ? a.beta[o] : 0.f;
+  const int sb = quarter;                // this warp's block of P and Z: columns 16 sb.., if not above the diagonal
+
+  // A piece is 64 columns of headdim of one head.  What the next piece needs is
+  // copied while this one is worked on: decays and largest magnitudes, E, D, V
+  // and dY, and, where this piece's operands have been used up, the states.
+  const bool v4 = a.P % 4 == 0, n4 = a.N % 4 == 0;
+  const auto copy_small = [&](int64_t h, int p0) {
+    if (h >= h1) return;
+    const int t = threadIdx.x;
+    if (t < kCheck) {
+      if (p0 == 0 && t < kC * nch) {
+        const Decays* d = decays(t >> 5, h);
+        cp_async4(sm100::smem_u32(intol + t), d->into + (t & 31));
+        cp_async4(sm100::smem_u32(outl + t), d->outof + (t & 31));
+        cp_async4(sm100::smem_u32(inv + t), d->inv + (t & 31));
+        cp_async4(sm100::smem_u32(bet + t), factors(t >> 5, h)->beta + (t & 31));
+        if ((t & 31) == 0) {
+          cp_async4(sm100::smem_u32(whole + (t >> 5)), &factors(t >> 5, h)->whole);
+          cp_async4(sm100::smem_u32(plain + (t >> 5)), &d->plain);
+        }
       }
-      double sum = c2[0] + c2[1];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += up;
-      }
-      const double end = __shfl_sync(0xffffffffu, sum, 31);
-      const double v[2] = {sum - c2[1], sum};
-      const bool plain = __all_sync(0xffffffffu, fabs(v[0]) <= 100.0 && fabs(v[1]) <= 100.0);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = 2 * lane + i;
-        cs[t] = v[i], into[t] = pow2_of(v[i]), outof[t] = pow2_of(end - v[i]), inv[t] = plain ? pow2_of(-v[i]) : 0.f;
-        bet[t] = b2[i];
-      }
-      if (lane == 0) plain_s = plain;
+    } else if (t < kCheck + 40) {
+      const int w = (t - kCheck) >> 3, c = ((t - kCheck) >> 2) & 1, i = p0 / 16 + (t & 3);
+      const float* src = w == 0 ? a.max_y : w == 1 ? a.max_e : w == 2 ? a.max_d : w == 3 ? a.max_s : a.max_ds;
+      const int64_t row = w < 3 ? (int64_t)(sl.chunk + c) * a.H + h : slot * a.H + h;
+      float* const to = &most[w][(t - kCheck) & 7];
+      if (i < a.pg && (c == 0 || (w < 3 && nch == 2))) cp_async4(sm100::smem_u32(to), src + row * a.pg + i);
+      else *to = 0.f;
     }
-    if (threadIdx.x < kCheck) sums[0][threadIdx.x] = sums[1][threadIdx.x] = 0.f;
-    const Factors* f = reinterpret_cast<const Factors*>(a.head + ((int64_t)sl.chunk * a.H + h) * HeadTiles<2>::kBytes +
-                                                        HeadTiles<2>::kF);
-    const Factors* f1 = reinterpret_cast<const Factors*>(reinterpret_cast<const char*>(f) +
-                                                         (nch == 2 ? a.H * HeadTiles<2>::kBytes : 0));
-    const float ik[2] = {f->ik, f1->ik}, iq[2] = {f->iq, f1->iq};
-    const int sb = quarter;  // this warp's block of P and Z: rows 16 mt.., columns 16 sb.., if not above the diagonal
+  };
+  const auto copy_rows = [&](int64_t h, int p0) {
+    if (h >= h1) return;
+    if constexpr (G::kAhead) {
+#pragma unroll
+      for (int x = 0; x < 64 * 16 / kGradThreads; ++x) {
+        const int t = (threadIdx.x >> 4) + (kGradThreads / 16) * x, p = (threadIdx.x & 15) * 4;
+        const int left = t < sl.n ? (int)(a.P - p0 - p) : 0;
+        const int64_t o = (((int64_t)sl.tok + t) * a.H + h) * a.P + p0 + p;
+        copy4(sm + G::kRawE + (t * 64 + p) * 4, a.e, o, left, v4);
+        copy4(sm + G::kRawD + (t * 64 + p) * 4, a.d, o, left, v4);
+        copy4(sm + G::kRawV + (t * 64 + p) * (int)sizeof(T), static_cast<const T*>(a.v), o, left, a.vec);
+        copy4(sm + G::kRawY + (t * 64 + p) * (int)sizeof(T), static_cast<const T*>(a.dy), o, left, a.vec);
+      }
+    }
+  };
+  constexpr int kSt = kPS * (NS / 4) / kGradThreads;  // fours of a state tile a thread holds
+  const auto state_at = [&](int i, int p0, int& p, int& n) {
+    const int at = threadIdx.x + i * kGradThreads;
+    p = at / (NS / 4), n = (at % (NS / 4)) * 4;
+    return p0 + p < a.P ? (int)(a.N - n0 - n) : 0;  // columns that exist
+  };
+  const auto copy_states = [&](int64_t h, int p0) {
+    if (h >= h1) return;
+    if constexpr (G::kAhead) {
+#pragma unroll
+      for (int i = 0; i < kSt; ++i) {
+        int p, n;
+        const int left = state_at(i, p0, p, n);
+        const int64_t o = ((slot * a.H + h) * a.P + p0 + p) * a.N + n0 + n;
+        const int to = (threadIdx.x + i * kGradThreads) * 16;
+        copy4(sm + G::kS + to, a.s, o, left, n4);
+        copy4(sm + G::kDS + to, a.ds, o, left, n4);
+      }
+    }
+  };
+  const float* sc = sl.fin == kInside ? a.s + (slot + 1) * a.H * a.P * a.N
+                    : a.s_fin && sl.fin >= 0 ? a.s_fin + (int64_t)sl.fin * a.H * a.P * a.N : nullptr;
+  copy_small(h0, 0);
+  copy_rows(h0, 0);
+  copy_states(h0, 0);
+  cp_async_commit();
+  for (int64_t h = h0; h < h1; ++h) {
     float P[2][4], Z[2][4], dqh[TN][4];
     clear(P);
     clear(Z);
     clear(dqh);
     float pi = 0.f;
     for (int p0 = 0; p0 < a.P; p0 += kPS) {
-      // the scales: largest magnitudes the walks left, by 16 rows of the
-      // state; a warp for each of the five
-      if (warp >= 1 && warp <= 5) {
-        const int i = p0 / 16 + (lane & 3), c = (lane >> 2) & 1;
-        const bool in = i < a.pg && (c == 0 || (warp <= 3 && nch == 2));
-        const float* src = warp == 1 ? a.max_y : warp == 2 ? a.max_e : warp == 3 ? a.max_d : warp == 4 ? a.max_s : a.max_ds;
-        const int64_t row = warp <= 3 ? (int64_t)(sl.chunk + c) * a.H + h : slot * a.H + h;
-        const float m = absmax_bits(in ? __float_as_uint(src[row * a.pg + i]) : 0u);
-        if (lane == 0) most[p0 / kPS & 1][warp - 1] = m;
-      }
-      __syncthreads();  // the factors are there; the previous slice's tiles are read
-      const float* mx = most[p0 / kPS & 1];
-      float iy, ie, id, is, ids;
-      const float sy = pow2_scale(mx[0], iy), se = pow2_scale(mx[1], ie), sd = pow2_scale(mx[2], id),
-                  ss = pow2_scale(mx[3], is), sds = pow2_scale(mx[4], ids);
-      const bool v4 = a.P % 4 == 0;
-      {  // all loads before the first use
-        constexpr int kIt = 64 * 16 / kGradThreads, kRows = kGradThreads / 16;
-        float e4[kIt][4], d4[kIt][4], u4[kIt][4], y4[kIt][4];
+      const int64_t hn = p0 + kPS < a.P ? h : h + 1;  // the next piece
+      const int pn = p0 + kPS < a.P ? p0 + kPS : 0;
+      cp_async_wait<0>();
+      __syncthreads();  // this piece's copies are there, the last one's operands are used up
+      if (threadIdx.x < kCheck) {
+        const int t = threadIdx.x;
+        if (p0 == 0) {
+          if (t >= kC * nch) intol[t] = outl[t] = inv[t] = 1.f, bet[t] = 0.f;
+          into[t] = intol[t] * (t >= kC && nch == 2 ? whole[0] : 1.f);
+          outof[t] = outl[t] * (t < kC && nch == 2 ? whole[1] : 1.f);
+          sums[0][t] = sums[1][t] = 0.f;
+        }
+      } else if (threadIdx.x < kCheck + 5) {
+        const int w = threadIdx.x - kCheck;
+        float m = 0.f;
 #pragma unroll
-        for (int x = 0; x < kIt; ++x) {
-          const int t = (threadIdx.x >> 4) + kRows * x, p = (threadIdx.x & 15) * 4;
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, most[w][i]);
+        scale[w] = pow2_scale(m, iscale[w]);
+      }
+      {  // the states to operands, and <dS, S_C>
+        float xs[kSt][4], xd[kSt][4], xc[kSt][4];
+#pragma unroll
+        for (int i = 0; i < kSt; ++i) {
+          int p, n;
+          const int left = state_at(i, p0, p, n);
+          const int64_t o = (h * a.P + p0 + p) * a.N + n0 + n;
+          get4(sc ? sc + o : a.s, sc ? left : 0, n4, xc[i]);
+          if constexpr (G::kAhead) {
+            get4(reinterpret_cast<const float*>(sm + G::kS) + (threadIdx.x + i * kGradThreads) * 4, xs[i]);
+            get4(reinterpret_cast<const float*>(sm + G::kDS) + (threadIdx.x + i * kGradThreads) * 4, xd[i]);
+          } else {
+            get4(a.s + slot * a.H * a.P * a.N + o, left, n4, xs[i]);
+            get4(a.ds + slot * a.H * a.P * a.N + o, left, n4, xd[i]);
+          }
+        }
+        __syncthreads();  // the copied tiles are read; factors and scales are there
+#pragma unroll
+        for (int i = 0; i < kSt; ++i) {
+          int p, n;
+          state_at(i, p0, p, n);
+          const uint32_t to = tile_off<NS>(p, n);
+          put4<2>(sm + G::kS, G::kTok, to, xs[i], scale[3]);
+          put4<TM>(sm + G::kDS, G::kTok, to, xd[i], scale[4]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pi = fmaf(xd[i][e], xc[i][e], pi);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 64 * 16 / kGradThreads; ++x) {  // E, D and dY to operands; d.e and d.v
+        const int t = (threadIdx.x >> 4) + (kGradThreads / 16) * x, p = (threadIdx.x & 15) * 4;
+        float e4[4], d4[4], u4[4], y4[4];
+        if constexpr (G::kAhead) {
+          get4(reinterpret_cast<const float*>(sm + G::kRawE) + t * 64 + p, e4);
+          get4(reinterpret_cast<const float*>(sm + G::kRawD) + t * 64 + p, d4);
+          get4(reinterpret_cast<const T*>(sm + G::kRawY) + t * 64 + p, y4);
+          get4(reinterpret_cast<const T*>(sm + G::kRawV) + t * 64 + p, u4);
+        } else {
           const int left = t < sl.n ? (int)(a.P - p0 - p) : 0;
           const int64_t o = (((int64_t)sl.tok + t) * a.H + h) * a.P + p0 + p;
-          get4(a.e + o, left, v4, e4[x]);
-          get4(a.d + o, left, v4, d4[x]);
-          get4(static_cast<const T*>(a.dy) + o, left, a.vec, y4[x]);
-          get4(static_cast<const T*>(a.v) + o, left, a.vec, u4[x]);
+          get4(a.e + o, left, v4, e4);
+          get4(a.d + o, left, v4, d4);
+          get4(static_cast<const T*>(a.dy) + o, left, a.vec, y4);
+          get4(static_cast<const T*>(a.v) + o, left, a.vec, u4);
         }
+        float de = 0.f, dv = 0.f;
 #pragma unroll
-        for (int x = 0; x < kIt; ++x) {
-          const int t = (threadIdx.x >> 4) + kRows * x, p = (threadIdx.x & 15) * 4;
-          float de = 0.f, dv = 0.f;
+        for (int i = 0; i < 4; ++i) de = fmaf(d4[i], e4[i], de), dv = fmaf(d4[i], u4[i], dv);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) de = fmaf(d4[x][i], e4[x][i], de), dv = fmaf(d4[x][i], u4[x][i], dv);
-#pragma unroll
-          for (int i = 8; i > 0; i >>= 1) {
-            de += __shfl_xor_sync(0xffffffffu, de, i);
-            dv += __shfl_xor_sync(0xffffffffu, dv, i);
-          }
-          if ((lane & 15) == 0) sums[0][t] += de, sums[1][t] += dv;  // one thread of its own for each t
-          const uint32_t to = tile_off<64>(t, p);
-          put4<2>(sm + G::kE, G::kSmall, to, e4[x], se);
-          put4<TM>(sm + G::kD, G::kSmall, to, d4[x], sd);
-          put4<TM>(sm + G::kY, G::kSmall, to, y4[x], sy);
+        for (int i = 8; i > 0; i >>= 1) {
+          de += __shfl_xor_sync(0xffffffffu, de, i);
+          dv += __shfl_xor_sync(0xffffffffu, dv, i);
         }
-      }
-      const bool n4 = a.N % 4 == 0;
-      const float* sc = sl.fin == kInside ? a.s + (slot + 1) * a.H * a.P * a.N
-                        : a.s_fin && sl.fin >= 0 ? a.s_fin + (int64_t)sl.fin * a.H * a.P * a.N : nullptr;
-      {
-        constexpr int kIt = kPS * (NS / 4) / kGradThreads;
-        float x[kIt][4], y[kIt][4], z[kIt][4];
-#pragma unroll
-        for (int i = 0; i < kIt; ++i) {
-          const int at = threadIdx.x + i * kGradThreads, p = at / (NS / 4), n = (at % (NS / 4)) * 4;
-          const int left = p0 + p < a.P ? (int)(a.N - n0 - n) : 0;
-          const int64_t o = (h * a.P + p0 + p) * a.N + n0 + n, ol = slot * a.H * a.P * a.N + o;
-          get4(a.s + ol, left, n4, x[i]);
-          get4(a.ds + ol, left, n4, y[i]);
-          get4(sc ? sc + o : a.s, sc ? left : 0, n4, z[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < kIt; ++i) {
-          const int at = threadIdx.x + i * kGradThreads, p = at / (NS / 4), n = (at % (NS / 4)) * 4;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) pi = fmaf(y[i][e], z[i][e], pi);
-          const uint32_t to = tile_off<NS>(p, n);
-          put4<2>(sm + G::kS, G::kTok, to, x[i], ss);
-          put4<TM>(sm + G::kDS, G::kTok, to, y[i], sds);
-        }
+        if ((lane & 15) == 0) sums[0][t] += de, sums[1][t] += dv;  // one thread of its own for each t
+        const uint32_t to = tile_off<64>(t, p);
+        put4<2>(sm + G::kE, G::kSmall, to, e4, scale[1]);
+        put4<TM>(sm + G::kD, G::kSmall, to, d4, scale[2]);
+        put4<TM>(sm + G::kY, G::kSmall, to, y4, scale[0]);
       }
       __syncthreads();
+      copy_rows(hn, pn);
+      const float iy = iscale[0], ie = iscale[1], id = iscale[2], is = iscale[3], ids = iscale[4];
       // dY E^T and D E^T, blocks of 16 tokens on and below the diagonal
       if (sb <= mt) {
         float x[2][4], z[2][4];
@@ -362,64 +446,84 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
       }
       float tmp[TN][4];
       const int nb = quarter * (NS / 4);
+      const float in0 = into[r0], in1 = into[r0 + 8], be0 = bet[r0], be1 = bet[r0 + 8];
       clear(tmp);
       product<TN, 64, false, TM, NS, 2>(tmp, smu + G::kY, G::kSmall, 16 * mt, smu + G::kS, G::kTok, nb, 0, kPS / 16, lane);
-      add_rows(dqh, tmp, a.scale * into[r0] * (iy * is), a.scale * into[r0 + 8] * (iy * is));
+      add_rows(dqh, tmp, a.scale * in0 * (iy * is), a.scale * in1 * (iy * is));
       clear(tmp);
       product<TN, 64, false, TM, NS, TM>(tmp, smu + G::kD, G::kSmall, 16 * mt, smu + G::kS, G::kTok, nb, 0, kPS / 16, lane);
-      add_rows(dk, tmp, -bet[r0] * into[r0] * (id * is), -bet[r0 + 8] * into[r0 + 8] * (id * is));
+      add_rows(dk, tmp, -be0 * in0 * (id * is), -be1 * in1 * (id * is));
       clear(tmp);
       product<TN, 64, false, TM, NS, TM>(tmp, smu + G::kE, G::kSmall, 16 * mt, smu + G::kDS, G::kTok, nb, 0, kPS / 16, lane);
-      add_rows(dk, tmp, bet[r0] * outof[r0] * (ie * ids), bet[r0 + 8] * outof[r0 + 8] * (ie * ids));
+      add_rows(dk, tmp, be0 * outof[r0] * (ie * ids), be1 * outof[r0 + 8] * (ie * ids));
+      if (hn == h) {  // another piece of this head
+        __syncthreads();
+        copy_small(hn, pn);
+        copy_states(hn, pn);
+        cp_async_commit();
+      }
     }
-    // P and Z with their decays; the scales of the chunks' k and q go with the
-    // token that is summed over
-    float m1 = 0.f, m2 = 0.f, m3 = 0.f;
+    // P and Z with their decays; the scale of the chunk's k or q goes with the
+    // token that is summed over.  A block's rows are in one chunk, its columns too.
+    const float kt = mt < 2 ? ik0 : ik1, ks = sb < 2 ? ik0 : ik1, qt = mt < 2 ? iq0 : iq1;
+    float m1 = 0.f, m3 = 0.f;
     if (sb <= mt) {
+      const bool cross = (mt >> 1) != (sb >> 1), simple = cross || plain[mt >> 1];
+      const float* cf = cross ? outl : inv;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int hh = 0; hh < 2; ++hh) {
+        const int t = r0 + 8 * hh;
+        const float rf = intol[t], bt = -bet[t];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int t = r0 + 8 * (e >> 1), s = 16 * sb + 8 * i + 2 * (lane & 3) + (e & 1);
-          float w = 0.f;
-          if (s <= t) w = (plain_s ? into[t] * inv[s] : pow2_of(cs[t] - cs[s])) * bet[s];
-          P[i][e] *= a.scale * w;
-          Z[i][e] *= s < t ? -bet[t] * w : 0.f;
-          m1 = fmaxf(m1, fabsf(P[i][e]) * ik[s >> 5]);
-          m2 = fmaxf(m2, fabsf(P[i][e]) * iq[t >> 5]);
-          m3 = fmaxf(m3, fabsf(Z[i][e]) * fmaxf(ik[t >> 5], ik[s >> 5]));
-        }
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int s = 16 * sb + 8 * i + 2 * (lane & 3) + e;
+            float w = rf * cf[s];
+            if (!simple && s <= t) w = pow2_of(decays(mt >> 1, h)->cs[t & 31] - decays(mt >> 1, h)->cs[s & 31]);
+            w = s <= t ? w * bet[s] : 0.f;
+            float& p = P[i][2 * hh + e];
+            float& z = Z[i][2 * hh + e];
+            p *= a.scale * w;
+            z = s < t ? z * (bt * w) : 0.f;
+            m1 = fmaxf(m1, fabsf(p)), m3 = fmaxf(m3, fabsf(z));
+          }
+      }
     }
-    m1 = absmax_bits(__float_as_uint(m1)), m2 = absmax_bits(__float_as_uint(m2)), m3 = absmax_bits(__float_as_uint(m3));
+    {
+      const float m2 = absmax_bits(__float_as_uint(m1 * qt));
+      m1 = absmax_bits(__float_as_uint(m1 * ks)), m3 = absmax_bits(__float_as_uint(m3 * fmaxf(kt, ks)));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) pi += __shfl_xor_sync(0xffffffffu, pi, o);
-    if (lane == 0) wmax[0][warp] = m1, wmax[1][warp] = m2, wmax[2][warp] = m3, wpi[warp] = pi;
-    __syncthreads();
-    m1 = m2 = m3 = 0.f;
-#pragma unroll
-    for (int i = 0; i < kGradWarps; ++i) m1 = fmaxf(m1, wmax[0][i]), m2 = fmaxf(m2, wmax[1][i]), m3 = fmaxf(m3, wmax[2][i]);
+      for (int o = 16; o > 0; o >>= 1) pi += __shfl_xor_sync(0xffffffffu, pi, o);
+      if (lane == 0) wmax[0][warp] = m1, wmax[1][warp] = m2, wmax[2][warp] = m3, wpi[warp] = pi;
+    }
+    __syncthreads();  // and the states' operands are used up
+    copy_states(h + 1, 0);
     float i1, i2, i3;
-    const float s1 = pow2_scale(m1, i1), s2 = pow2_scale(m2, i2), s3 = pow2_scale(m3, i3);
-    if (sb <= mt) {
+    {
+      m1 = lane < kGradWarps ? wmax[0][lane] : 0.f, m3 = lane < kGradWarps ? wmax[2][lane] : 0.f;
+      const float m2 = lane < kGradWarps ? wmax[1][lane] : 0.f;
+      const float s1 = pow2_scale(absmax_bits(__float_as_uint(m1)), i1), s2 = pow2_scale(absmax_bits(__float_as_uint(m2)), i2),
+                  s3 = pow2_scale(absmax_bits(__float_as_uint(m3)), i3);
+      if (sb <= mt) {
+        const float f1 = ks * s1, f2 = qt * s2, fa = kt * s3, fb = ks * s3;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int t = r0 + 8 * hh, s = 16 * sb + 8 * i + 2 * (lane & 3);
-          const uint32_t o = tile_off<64>(t, s);
-          const float ks = ik[s >> 5], kt = ik[t >> 5], qt = iq[t >> 5];
-          const float pa = P[i][2 * hh], pb = P[i][2 * hh + 1], za = Z[i][2 * hh], zb = Z[i][2 * hh + 1];
-          const auto put = [&](int at, bool two, float2 x) {
-            uint32_t hi, lo;
-            split2(x, hi, lo);
-            *reinterpret_cast<uint32_t*>(sm + at + o) = hi;
-            if (two) *reinterpret_cast<uint32_t*>(sm + at + G::kSmall + o) = lo;
-          };
-          put(G::kW1, true, mul2(pa * ks, pb * ks, s1));
-          put(G::kW2, TM == 2, mul2(pa * qt, pb * qt, s2));
-          put(G::kZa, TM == 2, mul2(za * kt, zb * kt, s3));
-          put(G::kZb, TM == 2, mul2(za * ks, zb * ks, s3));
-        }
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint32_t o = tile_off<64>(r0 + 8 * hh, 16 * sb + 8 * i + 2 * (lane & 3));
+            const auto put = [&](int at, bool two, float2 x) {
+              uint32_t hi, lo;
+              split2(x, hi, lo);
+              *reinterpret_cast<uint32_t*>(sm + at + o) = hi;
+              if (two) *reinterpret_cast<uint32_t*>(sm + at + G::kSmall + o) = lo;
+            };
+            put(G::kW1, true, mul2(P[i][2 * hh], P[i][2 * hh + 1], f1));
+            put(G::kW2, TM == 2, mul2(P[i][2 * hh], P[i][2 * hh + 1], f2));
+            put(G::kZa, TM == 2, mul2(Z[i][2 * hh], Z[i][2 * hh + 1], fa));
+            put(G::kZb, TM == 2, mul2(Z[i][2 * hh], Z[i][2 * hh + 1], fb));
+          }
+      }
     }
     __syncthreads();
     {
@@ -455,25 +559,29 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
         q0 += __shfl_xor_sync(0xffffffffu, q0, o);
         q1 += __shfl_xor_sync(0xffffffffu, q1, o);
       }
-      q0 *= iq[r0 >> 5], q1 *= iq[(r0 + 8) >> 5];
-      if ((lane & 3) == 0) sums[2 + quarter][r0] = q0, sums[2 + quarter][r0 + 8] = q1;
-      __syncthreads();
-      if (threadIdx.x < sl.n)
-        a.qdq[(int64_t)ns * a.part_stride + ((int64_t)sl.tok + threadIdx.x) * a.H + h] =
-            (sums[2][threadIdx.x] + sums[3][threadIdx.x]) + (sums[4][threadIdx.x] + sums[5][threadIdx.x]);
+      if ((lane & 3) == 0) sums[2 + quarter][r0] = q0 * qt, sums[2 + quarter][r0 + 8] = q1 * qt;
       add_rows(dq, dqh, 1.f, 1.f);
     }
-    if (ns == 0 && threadIdx.x < sl.n) {
-      const int64_t o = ((int64_t)sl.tok + threadIdx.x) * a.H + h;
-      a.dbeta[o] = sums[0][threadIdx.x];
-      a.dvv[o] = sums[1][threadIdx.x] * bet[threadIdx.x];
-    }
-    if (threadIdx.x == 0) {
+    __syncthreads();
+    if (threadIdx.x < sl.n) {
+      const int t = threadIdx.x;
+      const int64_t o = ((int64_t)sl.tok + t) * a.H + h;
+      a.qdq[(int64_t)ns * a.part_stride + o] = (sums[2][t] + sums[3][t]) + (sums[4][t] + sums[5][t]);
+      if (ns == 0) {
+        a.dbeta[o] = sums[0][t];
+        a.dvv[o] = sums[1][t] * bet[t];
+      }
+    } else if (threadIdx.x == kCheck) {
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < kGradWarps; ++i) s += wpi[i];
       a.pi[((int64_t)ns * a.slots_n + slot) * a.H + h] = s;
     }
+    if (h + 1 < h1) {
+      __syncthreads();  // the factors are used up
+      copy_small(h + 1, 0);
+    }
+    cp_async_commit();
   }
   // dq and dk: rows of the group, or this split's part of them
 #pragma unroll

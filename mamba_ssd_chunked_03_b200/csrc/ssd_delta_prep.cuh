@@ -48,6 +48,16 @@ struct alignas(16) Factors {
   float pad[2];
 };
 
+// What the gradients need of a chunk's decays besides (kept beside the reverse
+// walk's tiles).
+struct alignas(16) Decays {
+  double cs[kC];               // cumulative log2 decay
+  float into[kC], outof[kC];   // exp(cs), exp(cs_C - cs)
+  float inv[kC];               // 1 / exp(cs), if `plain`
+  int plain;                   // exp(cs_t - cs_s) is into_t inv_s
+  int pad[3];
+};
+
 // Sizes of the images, in bytes.
 constexpr int kSq = kC * kC * 2;  // a 32 x 32 fp16 tile
 template <typename T, int NT>
@@ -56,11 +66,13 @@ struct TokenTiles {  // a chunk's k, then q, terms of each: one set for a group
   static constexpr int kTile = kC * NT * 2;
   static constexpr int kBytes = 2 * kTerms * kTile;
 };
-// A head's: the inverse (hi, lo), M (terms), Factors.
-template <int MTERMS>
+// A head's: the inverse (hi, lo), M (terms), Factors; DECAYS: and, not copied by the walk, Decays.
+template <int MTERMS, bool DECAYS = false>
 struct HeadTiles {
   static constexpr int kM = 2 * kSq, kF = kM + MTERMS * kSq, kBytes = kF + (int)sizeof(Factors);
+  static constexpr int kStride = kBytes + (DECAYS ? (int)sizeof(Decays) : 0);
 };
+using RevTiles = HeadTiles<2, true>;
 static_assert(HeadTiles<1>::kBytes % 16 == 0, "16-byte copies");
 
 struct PrepArgs {
@@ -125,7 +137,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(const PrepArgs a) {
   constexpr int MT = REV || sizeof(T) == 4 ? 2 : 1;
   constexpr bool kFwdM = !REV;  // the backward's forward walk makes no y
   using HF = HeadTiles<kFwdM ? MT : 0>;
-  using HR = HeadTiles<2>;
+  using HR = RevTiles;
   constexpr int E = 16 / (int)sizeof(T), PC = NT / E, V = kC * NT / E / kPrepThreads;
   extern __shared__ __align__(128) char sm[];
   float* gk = reinterpret_cast<float*>(sm + X::kBytes);  // k k^T, q k^T: true values
@@ -272,7 +284,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(const PrepArgs a) {
     for (int dir = 0; dir < 2; ++dir) {
       if (dir == 0 ? !FWD : !REV) continue;
       const bool rev = dir == 1;
-      char* img = rev ? a.rev + (ch * a.H + h) * HR::kBytes : a.fwd + (ch * a.H + h) * HF::kBytes;
+      char* img = rev ? a.rev + (ch * a.H + h) * HR::kStride : a.fwd + (ch * a.H + h) * HF::kStride;
       Factors* f = reinterpret_cast<Factors*>(img + (rev ? HR::kF : HF::kF));
       __syncwarp();
       vb[lane] = rev ? inv : inv * bt;
@@ -339,6 +351,11 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(const PrepArgs a) {
         char* mi = img + (rev ? HR::kM : HF::kM);
         f->mu[lane] = store_row(t, lane, mi, (rev ? 2 : MT) == 2 ? mi + kSq : nullptr);
         f->qc[lane] = qc;
+        if (rev) {
+          Decays* d = reinterpret_cast<Decays*>(img + HR::kBytes);
+          d->cs[lane] = sum, d->into[lane] = into, d->outof[lane] = outof, d->inv[lane] = inv;
+          if (lane == 0) d->plain = plain;
+        }
       }
     }
   }

@@ -15,7 +15,7 @@ template <typename T, int NT>
 __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_rwalk(const WalkArgs a) {
   using B = Buffers<T, NT, true, 2>;
   using X = TokenTiles<T, NT>;
-  using Hd = HeadTiles<2>;
+  using Hd = RevTiles;
   constexpr int kTerms = X::kTerms;
   extern __shared__ __align__(128) char sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -26,9 +26,9 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_rwalk(con
   const int p_cta = slice * kP, p0 = p_cta + 16 * warp;
   const int cols = (int)(a.P - p_cta < kP ? a.P - p_cta : kP);
   const int rows = a.P - p0 < 16 ? (int)(a.P - p0) : 16;
-  const int64_t vstride = a.H * a.P, tstride = a.G * X::kBytes, hstride = a.H * Hd::kBytes;
+  const int64_t vstride = a.H * a.P, tstride = a.G * X::kBytes, hstride = a.H * Hd::kStride;
   const char* tok = a.tokens + (run.chunk * a.G + h / a.hpg) * X::kBytes;
-  const char* head = a.heads + (run.chunk * a.H + h) * Hd::kBytes;
+  const char* head = a.heads + (run.chunk * a.H + h) * Hd::kStride;
   const T* v = static_cast<const T*>(a.v) + (run.tok * a.H + h) * a.P + p_cta;
   float S[NT / 8][4];
   if (a.s0 && run.fin >= 0) {

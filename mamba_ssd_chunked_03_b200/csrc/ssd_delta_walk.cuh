@@ -469,9 +469,9 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(cons
   const int p_cta = slice * kP, p0 = p_cta + 16 * warp;
   const int cols = (int)(a.P - p_cta < kP ? a.P - p_cta : kP);
   const int rows = a.P - p0 < 16 ? (int)(a.P - p0) : 16;  // may be negative: nothing is read or written
-  const int64_t vstride = a.H * a.P, tstride = a.G * X::kBytes, hstride = a.H * Hd::kBytes;
+  const int64_t vstride = a.H * a.P, tstride = a.G * X::kBytes, hstride = a.H * Hd::kStride;
   const char* tok = a.tokens + (run.chunk * a.G + h / a.hpg) * X::kBytes;
-  const char* head = a.heads + (run.chunk * a.H + h) * Hd::kBytes;
+  const char* head = a.heads + (run.chunk * a.H + h) * Hd::kStride;
   const T* v = static_cast<const T*>(a.v) + (run.tok * a.H + h) * a.P + p_cta;
   float S[NT / 8][4];
   if (a.s0 && run.h0 >= 0) {

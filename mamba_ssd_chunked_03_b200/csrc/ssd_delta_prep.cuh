@@ -132,7 +132,7 @@ __device__ __forceinline__ float store_row(const float (&t)[kC], int lane, char*
 
 // FWD, REV: which walk's tiles are made; MT: terms of M.
 template <typename T, int NT, bool FWD, bool REV>
-__global__ void __launch_bounds__(kPrepThreads) k_delta_prep(const PrepArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, NT * sizeof(T) <= 256 ? 6 : 3) k_delta_prep(const PrepArgs a) {
   using X = TokenTiles<T, NT>;
   constexpr int MT = REV || sizeof(T) == 4 ? 2 : 1;
   constexpr bool kFwdM = !REV;  // the backward's forward walk makes no y
@@ -140,9 +140,10 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(const PrepArgs a) {
   using HR = RevTiles;
   constexpr int E = 16 / (int)sizeof(T), PC = NT / E, V = kC * NT / E / kPrepThreads;
   extern __shared__ __align__(128) char sm[];
-  float* gk = reinterpret_cast<float*>(sm + X::kBytes);  // k k^T, q k^T: true values
+  float* gk = reinterpret_cast<float*>(sm);  // k k^T, q k^T: true values
   float* gq = gk + kC * kGP;
-  float* at = gq + kC * kGP;                             // a warp's A, transposed
+  char* const tiles = sm + 2 * kC * kGP * 4;                // k and q; when their products are formed,
+  float* at = reinterpret_cast<float*>(tiles);              // a warp's A, transposed
   __shared__ float maxes[2][kPrepThreads / 32];
   __shared__ __align__(16) float col[kPrepThreads / 32][2][kC];
   __shared__ double css[kPrepThreads / 32][kC];
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(const PrepArgs a) {
     c.n = a.L - (int64_t)j * kC < kC ? (int)(a.L - (int64_t)j * kC) : kC;
   }
   if (c.n == 0) return;
-  const uint32_t smu = sm100::smem_u32(sm);
+  const uint32_t smu = sm100::smem_u32(tiles);
   float inv_k, inv_q;
   {  // the tiles of k and q: fp16, each scaled by its largest magnitude
     const int row0 = threadIdx.x / PC, cc = (threadIdx.x % PC) * E;
@@ -206,15 +207,15 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(const PrepArgs a) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) h[e] = pack2(__fmul2_rn(bf16x2(u[e]), make_float2(sc[w], sc[w])));
           const uint4 p = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(sm + o) = p;
+          *reinterpret_cast<uint4*>(tiles + o) = p;
           if (split == 0) *reinterpret_cast<uint4*>(out + o) = p;
         } else {
           uint32_t hi[2], lo[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             split2(mul2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]), sc[w]), hi[e], lo[e]);
-          *reinterpret_cast<uint2*>(sm + o) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(sm + o + X::kTile) = make_uint2(lo[0], lo[1]);
+          *reinterpret_cast<uint2*>(tiles + o) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(tiles + o + X::kTile) = make_uint2(lo[0], lo[1]);
           if (split == 0) {
             *reinterpret_cast<uint2*>(out + o) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2*>(out + o + X::kTile) = make_uint2(lo[0], lo[1]);
@@ -363,12 +364,14 @@ __global__ void __launch_bounds__(kPrepThreads) k_delta_prep(const PrepArgs a) {
 
 template <typename T, int NT, bool FWD, bool REV>
 cudaError_t launch_prep_nt(PrepArgs& a, int64_t chunks, cudaStream_t stream) {
-  constexpr int smem = TokenTiles<T, NT>::kBytes + (2 + kPrepThreads / 32) * kC * kGP * 4;
+  constexpr int kHeads = kPrepThreads / 32 * kC * kGP * 4, kTok = TokenTiles<T, NT>::kBytes;
+  constexpr int smem = (kTok > kHeads ? kTok : kHeads) + 2 * kC * kGP * 4;
   static_assert(smem <= 227 * 1024, "shared memory");
-  // Heads of a group in one CTA share its tiles and products; with few chunks
-  // they are spread until every SM has a few CTAs, a head a warp at the least.
+  // Heads of a group in one CTA share its tiles and products; they are spread
+  // until every SM has some 24 CTAs, five at a time, so that the last ones
+  // leave little idle, a head a warp at the least.
   const int64_t units = chunks * a.G, most = (a.hpg + 3) / 4;
-  int64_t splits = (6 * 148 + units - 1) / units;
+  int64_t splits = (24 * 148 + units - 1) / units;
   splits = splits < 1 ? 1 : splits > most ? most : splits;
   a.heads = (int)((a.hpg + splits - 1) / splits);
   a.splits = (int)((a.hpg + a.heads - 1) / a.heads);

@@ -3,9 +3,9 @@
 // last CTAs to start are short), and lists the ids that do not occur, whose
 // final states the main kernel zeroes.
 //
-// Bound by latency: the ids are read twice, 32 at a time per warp with eight
-// loads in flight, each warp over its own contiguous range.  16384 ids take
-// about 8 us.
+// Bound by latency, a chain of a few global accesses between barriers: the ids
+// are read 32 at a time per warp with eight loads in flight, each warp over its
+// own contiguous range, and once only up to 65536 of them.
 #include <vector>
 
 #include "ssd_delta.cuh"
@@ -18,8 +18,11 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kRanked = 2048;  // runs up to which they are ranked (quadratic work)
 
-__device__ __forceinline__ bool starts(const int32_t* seq, int64_t i, int64_t L) {
-  return i % L == 0 || seq[i] != seq[i - 1];
+// Whether a run starts at token i (32-bit arithmetic: a 64-bit remainder for
+// each id took most of the kernel's time).
+__device__ __forceinline__ bool starts(const int32_t* seq, uint32_t i, uint32_t L, bool rows) {
+  if (i == 0 || (rows && i % L == 0)) return true;
+  return seq[i] != seq[i - 1];
 }
 
 __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restrict__ seq, int64_t n, int64_t L,
@@ -28,12 +31,37 @@ __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restri
   Run* const runs = out.runs;
   Chunk* const chunks = out.chunks;
   Slot* const slots = out.slots;
-  int32_t* const first = out.first;
   int32_t* const present = out.present;
   __shared__ int warp_count[32];
   __shared__ int total, absent;
-  __shared__ int lens[kRanked];
+  __shared__ int lens[kRanked], starts_s[kRanked + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool rows = L < n, small = cap <= kRanked;
+  int32_t* const first = small ? starts_s : out.first;
+  const int64_t per = ((n + 31) / 32 + 31) / 32 * 32;  // ids per warp, a multiple of 32
+  const int64_t i0 = warp * per, i1 = i0 + per < n ? i0 + per : n;
+  // eight flags of this lane for each 256 ids of the warp; those of the first
+  // 2048 are kept for the second pass
+  const auto flags = [&](int64_t i) {
+    uint32_t f = 0;
+    bool s[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      s[u] = i + 32 * u + lane < i1 && starts(seq, (uint32_t)(i + 32 * u + lane), (uint32_t)L, rows);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) f |= (uint32_t)s[u] << u;
+    return f;
+  };
+  uint64_t kept = 0;
+  int count = 0;
+  for (int64_t i = i0, it = 0; i < i1; i += 256, ++it) {
+    const uint32_t f = flags(i);
+    if (it < 8) kept |= (uint64_t)f << (8 * it);
+    count += __popc(f);
+  }
+  count = __reduce_add_sync(0xffffffffu, count);
+  if (lane == 0) warp_count[warp] = count;
+  if (threadIdx.x == 0) absent = 0;
   for (int64_t i = threadIdx.x; i < cap; i += kThreads) {
     present[i] = 0;
     Run r = {};
@@ -42,39 +70,28 @@ __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restri
   }
   for (int64_t i = threadIdx.x; i < places; i += kThreads) chunks[i] = Chunk{0, 0};
   for (int64_t i = threadIdx.x; i < checks; i += kThreads) slots[i] = Slot{0, 0, 0, kInside, kInside};
-  const int64_t per = ((n + 31) / 32 + 31) / 32 * 32;  // ids per warp, a multiple of 32
-  const int64_t i0 = warp * per, i1 = i0 + per < n ? i0 + per : n;
-  int count = 0;
-  for (int64_t i = i0; i < i1; i += 256) {
-    bool s[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) s[u] = i + 32 * u + lane < i1 && starts(seq, i + 32 * u + lane, L);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) count += __popc(__ballot_sync(0xffffffffu, s[u]));
-  }
-  if (lane == 0) warp_count[warp] = count;
-  if (threadIdx.x == 0) absent = 0;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int sum = 0;
-    for (int w = 0; w < 32; ++w) {
-      const int c = warp_count[w];
-      warp_count[w] = sum;
-      sum += c;
+  if (warp == 0) {
+    const int c = warp_count[lane];
+    int sum = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += up;
     }
-    total = sum;
+    warp_count[lane] = sum - c;
+    if (lane == 31) total = sum;
   }
   __syncthreads();
   int64_t at = warp_count[warp];
-  for (int64_t i = i0; i < i1; i += 256) {
-    bool s[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) s[u] = i + 32 * u + lane < i1 && starts(seq, i + 32 * u + lane, L);
+  for (int64_t i = i0, it = 0; i < i1; i += 256, ++it) {
+    const uint32_t f = it < 8 ? (uint32_t)(kept >> (8 * it)) & 255u : flags(i);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const uint32_t m = __ballot_sync(0xffffffffu, s[u]);
+      const bool st = (f >> u) & 1;
+      const uint32_t m = __ballot_sync(0xffffffffu, st);
       const int64_t k = at + __popc(m & ((1u << lane) - 1u));
-      if (s[u] && k <= cap) first[k] = (int32_t)(i + 32 * u + lane);
+      if (st && k <= cap) first[k] = (int32_t)(i + 32 * u + lane);
       at += __popc(m);
     }
   }

@@ -43,32 +43,52 @@ struct Args {
   float* stat;  // wide rows: [rows][2] mean, rstd
 };
 
-// E consecutive elements as they are loaded and stored
+// Arithmetic on one value or on two at once (half the instructions).
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma_(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma_(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float total(float a) { return a; }
+__device__ __forceinline__ float total(float2 a) { return a.x + a.y; }
+template <typename V>
+__device__ __forceinline__ V all(float v);
+template <>
+__device__ __forceinline__ float all<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float2 all<float2>(float v) { return make_float2(v, v); }
+
+// E consecutive elements as they are loaded and stored, and as EV values of type V.
 template <typename T, int E>
 struct Pack;
 template <>
 struct Pack<float, 4> {
+  using V = float2;
   float4 r;
   __device__ __forceinline__ void load(const float* p) { r = __ldcs(reinterpret_cast<const float4*>(p)); }
-  __device__ __forceinline__ void get(float (&f)[4]) const { f[0] = r.x, f[1] = r.y, f[2] = r.z, f[3] = r.w; }
-  static __device__ __forceinline__ void store(float* p, const float (&f)[4]) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  __device__ __forceinline__ void get(float2 (&f)[2]) const { f[0] = make_float2(r.x, r.y), f[1] = make_float2(r.z, r.w); }
+  __device__ __forceinline__ void zero() { r = make_float4(0.f, 0.f, 0.f, 0.f); }
+  static __device__ __forceinline__ void store(float* p, const float2 (&f)[2]) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
   }
 };
 template <>
 struct Pack<__nv_bfloat16, 8> {
+  using V = float2;
   uint4 r;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
+  __device__ __forceinline__ void get(float2 (&f)[4]) const {
     const uint32_t u[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(u[i] << 16), f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
+  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float2 (&f)[4]) {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      const __nv_bfloat162 h = __float22bfloat162_rn(f[i]);
       u[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
@@ -76,16 +96,20 @@ struct Pack<__nv_bfloat16, 8> {
 };
 template <>
 struct Pack<float, 1> {
+  using V = float;
   float r;
   __device__ __forceinline__ void load(const float* p) { r = __ldcs(p); }
   __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = r; }
+  __device__ __forceinline__ void zero() { r = 0.f; }
   static __device__ __forceinline__ void store(float* p, const float (&f)[1]) { *p = f[0]; }
 };
 template <>
 struct Pack<__nv_bfloat16, 1> {
+  using V = float;
   __nv_bfloat16 r;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *p; }
   __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = __bfloat162float(r); }
+  __device__ __forceinline__ void zero() { r = __float2bfloat16_rn(0.f); }
   static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[1]) { *p = __float2bfloat16_rn(f[0]); }
 };
 
@@ -96,8 +120,20 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bf
 
 // The hardware exponential and an approximate divide: off by a few 2^-23.
 __device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
-// z sigmoid(z); 0 at z = -inf
-__device__ __forceinline__ float silu(float v) { return v < -1e30f ? 0.f : v * sigmoid(v); }
+// The gate bounded below where SiLU and its derivative are zero: -inf would
+// give 0 x inf.  NaN stays NaN.
+__device__ __forceinline__ float bounded(float v) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(v) : "f"(-1e30f));
+  return v;
+}
+__device__ __forceinline__ float2 bounded(float2 v) { return make_float2(bounded(v.x), bounded(v.y)); }
+__device__ __forceinline__ float2 sigmoid(float2 v) { return make_float2(sigmoid(v.x), sigmoid(v.y)); }
+// z sigmoid(z)
+__device__ __forceinline__ float silu(float v) {
+  v = bounded(v);
+  return v * sigmoid(v);
+}
+__device__ __forceinline__ float2 silu(float2 v) { return make_float2(silu(v.x), silu(v.y)); }
 
 // Sums of N values over the GT threads of a group (GT > 32: the CTA's threads,
 // however many), the same bits in each of them.
@@ -143,101 +179,111 @@ __global__ void __launch_bounds__(BT, MINB) k_norm(const Args a) {
   const int64_t cols = a.cols;
   const float inv_cols = 1.f / (float)cols;
   const auto col = [&](int v) { return (int64_t)(v * gt + l) * E; };
-  float w[VPL][E], b[VPL][E], dw[VPL][E], db[VPL][E];
+  using V = typename Pk::V;
+  constexpr int EV = E * (int)sizeof(float) / (int)sizeof(V);  // values of type V
+  V w[VPL][EV], b[VPL][EV], dw[VPL][EV], db[VPL][EV];
+  Pk xr[VPL], zr[VPL], dr[VPL];  // zeros for ever where the row has no columns
 #pragma unroll
-  for (int v = 0; v < VPL; ++v)
+  for (int v = 0; v < VPL; ++v) {
+    float wv[E], bv[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const bool in = col(v) < cols;
-      w[v][e] = a.w && in ? a.w[col(v) + e] : 1.f;
-      b[v][e] = a.b && in ? a.b[col(v) + e] : 0.f;
-      dw[v][e] = db[v][e] = 0.f;
+      wv[e] = a.w && in ? a.w[col(v) + e] : 1.f;
+      bv[e] = a.b && in ? a.b[col(v) + e] : 0.f;
     }
-  Pk xr[VPL], zr[VPL], dr[VPL];
-  const auto fetch = [&](int64_t r) {
-    if (r >= a.rows) return;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v)
-      if (col(v) < cols) {
-        xr[v].load(static_cast<const T*>(a.x) + r * cols + col(v));
-        if constexpr (GATE) zr[v].load(static_cast<const T*>(a.z) + r * cols + col(v));
-        if constexpr (BWD) dr[v].load(static_cast<const T*>(a.dout) + r * cols + col(v));
+    for (int e = 0; e < EV; ++e) {
+      w[v][e] = *reinterpret_cast<const V*>(wv + e * (E / EV)), b[v][e] = *reinterpret_cast<const V*>(bv + e * (E / EV));
+      dw[v][e] = db[v][e] = all<V>(0.f);
+    }
+    xr[v].zero(), zr[v].zero(), dr[v].zero();
+  }
+  const auto fetch = [&](int64_t r) {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      if (r < a.rows) {
+        if (col(v) < cols) {
+          xr[v].load(static_cast<const T*>(a.x) + r * cols + col(v));
+          if constexpr (GATE) zr[v].load(static_cast<const T*>(a.z) + r * cols + col(v));
+          if constexpr (BWD) dr[v].load(static_cast<const T*>(a.dout) + r * cols + col(v));
+        }
+      } else if constexpr (BWD) {
+        dr[v].zero();  // no such row: it must not count
       }
+    }
   };
   const int64_t stride = (int64_t)gridDim.x * GC;
   fetch((int64_t)blockIdx.x * GC + g);
   for (int64_t r0 = (int64_t)blockIdx.x * GC; r0 < a.rows; r0 += stride) {  // the same trips for all threads
     const int64_t r = r0 + g;
     const bool live = r < a.rows;
-    float x[VPL][E], z[VPL][E], d[VPL][E];  // x - mean, the gate, and dout: then dout SiLU(z)
-    float s0[1] = {0.f}, sq[1] = {0.f};
+    V x[VPL][EV], z[VPL][EV], d[VPL][EV];  // x - mean, the gate, and dout: then dout SiLU(z)
+    V s0 = all<V>(0.f), sq = all<V>(0.f);
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      const bool in = live && col(v) < cols;
       xr[v].get(x[v]);
       if constexpr (GATE) zr[v].get(z[v]);
       if constexpr (BWD) dr[v].get(d[v]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        x[v][e] = in ? x[v][e] : 0.f;
-        if constexpr (GATE) z[v][e] = in ? z[v][e] : 0.f;
-        if constexpr (BWD) d[v][e] = in ? d[v][e] : 0.f;
-        s0[0] += x[v][e];
-      }
+      for (int e = 0; e < EV; ++e) s0 = add(s0, x[v][e]);
     }
     fetch(r + stride);
-    sum(s0);
-    const float mean = s0[0] * inv_cols;
+    float t[1] = {total(s0)};
+    sum(t);
+    const float mean = t[0] * inv_cols;
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        x[v][e] = col(v) < cols ? x[v][e] - mean : 0.f;
-        sq[0] = fmaf(x[v][e], x[v][e], sq[0]);
+      for (int e = 0; e < EV; ++e) {
+        x[v][e] = add(x[v][e], all<V>(col(v) < cols ? -mean : 0.f));
+        sq = fma_(x[v][e], x[v][e], sq);
       }
-    sum(sq);
-    const float rstd = 1.f / sqrtf(fmaf(sq[0], inv_cols, a.eps));
+    t[0] = total(sq);
+    sum(t);
+    const float rstd = live ? 1.f / sqrtf(fmaf(t[0], inv_cols, a.eps)) : 0.f;
     if constexpr (!BWD) {
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
-        float y[E];
+        V y[EV];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          y[e] = fmaf(x[v][e] * rstd, w[v][e], b[v][e]);
-          if constexpr (GATE) y[e] *= silu(z[v][e]);
+        for (int e = 0; e < EV; ++e) {
+          y[e] = fma_(mul(x[v][e], all<V>(rstd)), w[v][e], b[v][e]);
+          if constexpr (GATE) y[e] = mul(y[e], silu(z[v][e]));
         }
         if (live && col(v) < cols) Pk::store(static_cast<T*>(a.out) + r * cols + col(v), y);
       }
     } else {
-      float m[2] = {0.f, 0.f};
+      V p1 = all<V>(0.f), p2 = all<V>(0.f);
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
-        float dz[E];
+        V dz[EV];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float n = x[v][e] * rstd;
-          float h = d[v][e];
-          if constexpr (GATE) {
-            const float sg = sigmoid(z[v][e]);
-            dz[e] = h * fmaf(n, w[v][e], b[v][e]) * (sg * fmaf(z[v][e], 1.f - sg, 1.f));
-            h *= z[v][e] * sg;
+        for (int e = 0; e < EV; ++e) {
+          x[v][e] = mul(x[v][e], all<V>(rstd));
+          V h = d[v][e];
+          if constexpr (GATE) {  // SiLU' = s + z s (1 - s)
+            const V zb = bounded(z[v][e]), sg = sigmoid(zb), zs = mul(zb, sg);
+            dz[e] = mul(mul(h, fma_(x[v][e], w[v][e], b[v][e])), fma_(zs, fma_(sg, all<V>(-1.f), all<V>(1.f)), sg));
+            h = mul(h, zs);
           }
-          dw[v][e] = fmaf(h, n, dw[v][e]);
-          db[v][e] += h;
-          d[v][e] = h * w[v][e];
-          m[0] += d[v][e];
-          m[1] = fmaf(d[v][e], n, m[1]);
+          dw[v][e] = fma_(h, x[v][e], dw[v][e]);
+          db[v][e] = add(db[v][e], h);
+          d[v][e] = mul(h, w[v][e]);
+          p1 = add(p1, d[v][e]);
+          p2 = fma_(d[v][e], x[v][e], p2);
         }
         if constexpr (GATE)
           if (live && col(v) < cols) Pk::store(static_cast<T*>(a.dz) + r * cols + col(v), dz);
       }
+      float m[2] = {total(p1), total(p2)};
       sum(m);
-      const float m1 = m[0] * inv_cols, m2 = m[1] * inv_cols * rstd;
+      const V m1 = all<V>(-m[0] * inv_cols), m2 = all<V>(-m[1] * inv_cols);
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
-        float y[E];
+        V y[EV];
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = rstd * (fmaf(-x[v][e], m2, d[v][e]) - m1);
+        for (int e = 0; e < EV; ++e) y[e] = mul(all<V>(rstd), add(fma_(x[v][e], m2, d[v][e]), m1));
         if (live && col(v) < cols) Pk::store(static_cast<T*>(a.out) + r * cols + col(v), y);
       }
     }
@@ -247,12 +293,13 @@ __global__ void __launch_bounds__(BT, MINB) k_norm(const Args a) {
     // the CTA's groups added in order, one set of partial sums a CTA
     float* pw = a.part + blockIdx.x * cols;
     float* pb = pw + (int64_t)kParts * cols;
+    const auto at = [](const V (&x)[EV], int e) { return reinterpret_cast<const float*>(&x)[e]; };
     if constexpr (GC == 1) {
 #pragma unroll
       for (int v = 0; v < VPL; ++v)
         if (col(v) < cols) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) pw[col(v) + e] = dw[v][e], pb[col(v) + e] = db[v][e];
+          for (int e = 0; e < E; ++e) pw[col(v) + e] = at(dw[v], e), pb[col(v) + e] = at(db[v], e);
         }
     } else {
       // groups of a warp by shuffles, then the warps through shared memory
@@ -262,7 +309,7 @@ __global__ void __launch_bounds__(BT, MINB) k_norm(const Args a) {
         __syncthreads();
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          float p = dw[v][e], q = db[v][e];
+          float p = at(dw[v], e), q = at(db[v], e);
 #pragma unroll
           for (int o = GT; o < 32; o <<= 1) {
             p += __shfl_xor_sync(0xffffffffu, p, o);
@@ -284,6 +331,11 @@ __global__ void __launch_bounds__(BT, MINB) k_norm(const Args a) {
   }
 }
 
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+               : "memory");
+}
+
 // Rows of bf16 that take a CTA.
 //
 // Such a row costs a barrier for every sum that waits for another one, so all
@@ -292,17 +344,31 @@ __global__ void __launch_bounds__(BT, MINB) k_norm(const Args a) {
 // mean(x - K)^2.  K is off the mean by at most sqrt(cols / 8) deviations, since
 // its elements are part of the row, and by less than one in all but contrived
 // rows; what cancels in var is then cols / 8 x 2^-24 at the very most, far
-// below the rounding of the outputs.  The row stays packed in registers and is
-// unpacked again after the sums; weight and bias lie in shared memory: that
-// leaves room for a second CTA's rows.
+// below the rounding of the outputs.  A thread copies its packs of the next
+// rows into a ring of its own in shared memory, where a second look at them
+// after the sums costs nothing; weight and bias lie there too.  That leaves the
+// registers to the column sums, and room for two rows at a time where a row has
+// two tensors at most: what takes the time is the chain of a row's sums through
+// the barrier, and two rows share one.  (16384 rows of 5120, backward: 138 us
+// with rows held in registers, 122 us from the ring one at a time.)
+template <int VPL, bool BWD, bool GATE>
+struct RowRing {
+  static constexpr int kTensors = 1 + GATE + BWD;
+  static constexpr int kRows = kTensors == 3 ? 1 : 2;  // at a time; as many again are on their way
+  static constexpr size_t bytes(int threads, int64_t cols) {
+    return (size_t)2 * kRows * kTensors * VPL * threads * 16 + (size_t)cols * (BWD && !GATE ? 4 : 8);
+  }
+};
 template <int VPL, int BT, int MINB, bool BWD, bool GATE>
 __global__ void __launch_bounds__(BT, MINB) k_norm_row(const Args a) {
   using T = __nv_bfloat16;
   constexpr int E = 8;
   using Pk = Pack<T, E>;
-  extern __shared__ __align__(16) float wb[];  // weight, bias
-  __shared__ float4 red[2][kMostThreads / 32];
-  GroupSum<64> sum{red};
+  using R = RowRing<VPL, BWD, GATE>;
+  extern __shared__ __align__(16) uint4 ring[];  // [row][tensor][pack][thread]
+  constexpr int NR = R::kRows, NS = BWD ? 4 : 2;
+  float* const wb = reinterpret_cast<float*>(ring + 2 * NR * R::kTensors * VPL * blockDim.x);  // weight, bias
+  __shared__ float4 red[2][NR][kMostThreads / 32];  // two sets, taken in turn
   const int l = threadIdx.x, gt = blockDim.x, cols = (int)a.cols;
   const float inv_cols = 1.f / (float)cols;
   const auto col = [&](int v) { return (v * gt + l) * E; };
@@ -311,104 +377,153 @@ __global__ void __launch_bounds__(BT, MINB) k_norm_row(const Args a) {
     if constexpr (GATE || !BWD) wb[cols + c] = a.b ? a.b[c] : 0.f;
   }
   __syncthreads();
-  const auto weights = [&](int c, float (&w)[E]) {
+  using V = float2;
+  constexpr int EV = E / 2;
+  const auto weights = [&](int c, V (&w)[EV]) {
     const float4 p = *reinterpret_cast<const float4*>(wb + c), q = *reinterpret_cast<const float4*>(wb + c + 4);
-    w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w, w[4] = q.x, w[5] = q.y, w[6] = q.z, w[7] = q.w;
+    w[0] = make_float2(p.x, p.y), w[1] = make_float2(p.z, p.w), w[2] = make_float2(q.x, q.y), w[3] = make_float2(q.z, q.w);
   };
-  float dw[BWD ? VPL : 1][E], db[BWD ? VPL : 1][E];
+  V dw[BWD ? VPL : 1][EV], db[BWD ? VPL : 1][EV];
 #pragma unroll
   for (int v = 0; v < (BWD ? VPL : 1); ++v)
 #pragma unroll
-    for (int e = 0; e < E; ++e) dw[v][e] = db[v][e] = 0.f;
-  Pk xn[VPL], zn[VPL], dn[VPL], kn;
-  const auto fetch = [&](int64_t r) {
-    if (r >= a.rows) return;
-    const int64_t o = r * cols;
-    kn.load(static_cast<const T*>(a.x) + o);
+    for (int e = 0; e < EV; ++e) dw[v][e] = db[v][e] = all<V>(0.f);
+  // x, dout, z: tensor t of row q of the rows at hand (set 0 or 1)
+  const auto place = [&](int set, int q, int t, int v) { return ring + (((set * NR + q) * R::kTensors + t) * VPL + v) * gt + l; };
+  const auto fetch = [&](int64_t r0, int set) {
 #pragma unroll
-    for (int v = 0; v < VPL; ++v)
-      if (col(v) < cols) {
-        xn[v].load(static_cast<const T*>(a.x) + o + col(v));
-        if constexpr (GATE) zn[v].load(static_cast<const T*>(a.z) + o + col(v));
-        if constexpr (BWD) dn[v].load(static_cast<const T*>(a.dout) + o + col(v));
-      }
+    for (int q = 0; q < NR; ++q) {
+      const int64_t r = r0 + (int64_t)q * gridDim.x, o = r * cols;
+      if (r >= a.rows) continue;
+#pragma unroll
+      for (int v = 0; v < VPL; ++v)
+        if (col(v) < cols) {
+          copy16(place(set, q, 0, v), static_cast<const T*>(a.x) + o + col(v));
+          if constexpr (BWD) copy16(place(set, q, 1, v), static_cast<const T*>(a.dout) + o + col(v));
+          if constexpr (GATE) copy16(place(set, q, 1 + BWD, v), static_cast<const T*>(a.z) + o + col(v));
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  fetch(blockIdx.x);
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    Pk xr[VPL], zr[VPL], dr[VPL];
-    float K = 0.f;
-    {
-      float k[E];
-      kn.get(k);
+  Pk kn[NR];
+  const auto first = [&](int64_t r0) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) K += k[e];
-      K *= 1.f / E;
+    for (int q = 0; q < NR; ++q) {
+      const int64_t r = r0 + (int64_t)q * gridDim.x;
+      if (r < a.rows) kn[q].load(static_cast<const T*>(a.x) + r * cols);
+      else kn[q].zero();
     }
+  };
+  const int64_t step = (int64_t)NR * gridDim.x;
+  first(blockIdx.x);
+  fetch(blockIdx.x, 0);
+  int set = 0;
+  for (int64_t r0 = blockIdx.x; r0 < a.rows; r0 += step, set ^= 1) {
+    fetch(r0 + step, set ^ 1);
+    float K[NR];
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      xr[v] = xn[v];
-      if constexpr (GATE) zr[v] = zn[v];
-      if constexpr (BWD) dr[v] = dn[v];
+    for (int q = 0; q < NR; ++q) {
+      V k[EV];
+      kn[q].get(k);
+      K[q] = total(add(add(k[0], k[1]), add(k[2], k[3]))) * (1.f / E);
     }
-    fetch(r + gridDim.x);
-    float t[BWD ? 4 : 2] = {};
+    first(r0 + step);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const auto see = [&](int q, int t, int v, V (&f)[EV]) {
+      Pk p;
+      p.r = *place(set, q, t, v);
+      p.get(f);
+    };
+    float t[NR][NS];
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      if (col(v) >= cols) continue;
-      float x[E], d[E], z[E], w[E];
-      xr[v].get(x);
-      if constexpr (BWD) {
-        dr[v].get(d);
-        weights(col(v), w);
-      }
-      if constexpr (BWD && GATE) zr[v].get(z);
+    for (int q = 0; q < NR; ++q) {
+      V p0 = all<V>(0.f), p1 = p0, p2 = p0, p3 = p0;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        x[e] -= K;
-        t[0] += x[e];
-        t[1] = fmaf(x[e], x[e], t[1]);
+      for (int v = 0; v < VPL; ++v) {
+        if (col(v) >= cols || r0 + (int64_t)q * gridDim.x >= a.rows) continue;
+        V x[EV], d[EV], z[EV], w[EV];
+        see(q, 0, v, x);
         if constexpr (BWD) {
-          float h = d[e] * w[e];
-          if constexpr (GATE) h *= z[e] * sigmoid(z[e]);
-          t[2] += h;
-          t[3] = fmaf(h, x[e], t[3]);
+          see(q, 1, v, d);
+          weights(col(v), w);
         }
+        if constexpr (BWD && GATE) see(q, 1 + BWD, v, z);
+#pragma unroll
+        for (int e = 0; e < EV; ++e) {
+          x[e] = add(x[e], all<V>(-K[q]));
+          p0 = add(p0, x[e]);
+          p1 = fma_(x[e], x[e], p1);
+          if constexpr (BWD) {
+            V h = mul(d[e], w[e]);
+            if constexpr (GATE) h = mul(h, silu(z[e]));
+            p2 = add(p2, h);
+            p3 = fma_(h, x[e], p3);
+          }
+        }
+      }
+      t[q][0] = total(p0), t[q][1] = total(p1);
+      if constexpr (BWD) t[q][2] = total(p2), t[q][3] = total(p3);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int q = 0; q < NR; ++q)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) t[q][i] += __shfl_xor_sync(0xffffffffu, t[q][i], o);
+    if ((l & 31) == 0) {
+#pragma unroll
+      for (int q = 0; q < NR; ++q) red[set][q][l >> 5] = make_float4(t[q][0], t[q][1], t[q][NS - 2], t[q][NS - 1]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < NR; ++q) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) t[q][i] = 0.f;
+#pragma unroll 5
+      for (int i = 0; i < (gt >> 5); ++i) {
+        const float4 x = red[set][q][i];
+        t[q][0] += x.x, t[q][1] += x.y;
+        if constexpr (BWD) t[q][2] += x.z, t[q][3] += x.w;
       }
     }
-    sum(t);
-    const float dm = t[0] * inv_cols, mean = K + dm;
-    const float rstd = 1.f / sqrtf(fmaxf(fmaf(t[1], inv_cols, -dm * dm), 0.f) + a.eps);
-    float m1 = 0.f, m2 = 0.f;
-    if constexpr (BWD) m1 = t[2] * inv_cols, m2 = rstd * (t[3] - dm * t[2]) * inv_cols;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      if (col(v) >= cols) continue;
-      float x[E], d[E], z[E], w[E], b[E], dz[E];
-      xr[v].get(x);
-      if constexpr (BWD) dr[v].get(d);
-      if constexpr (GATE) zr[v].get(z);
-      weights(col(v), w);
-      if constexpr (GATE || !BWD) weights(cols + col(v), b);
+    for (int q = 0; q < NR; ++q) {
+      const int64_t r = r0 + (int64_t)q * gridDim.x;
+      if (r >= a.rows) continue;
+      const float dm = t[q][0] * inv_cols, mean = K[q] + dm;
+      const float rstd = 1.f / sqrtf(fmaxf(fmaf(t[q][1], inv_cols, -dm * dm), 0.f) + a.eps);
+      float m1 = 0.f, m2 = 0.f;
+      if constexpr (BWD) m1 = t[q][2] * inv_cols, m2 = rstd * (t[q][3] - dm * t[q][2]) * inv_cols;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float n = (x[e] - mean) * rstd;
-        if constexpr (!BWD) {
-          x[e] = fmaf(n, w[e], b[e]);
-          if constexpr (GATE) x[e] *= silu(z[e]);
-        } else {
-          float h = d[e];
-          if constexpr (GATE) {
-            const float sg = sigmoid(z[e]);
-            dz[e] = h * fmaf(n, w[e], b[e]) * (sg * fmaf(z[e], 1.f - sg, 1.f));
-            h *= z[e] * sg;
+      for (int v = 0; v < VPL; ++v) {
+        if (col(v) >= cols) continue;
+        V x[EV], d[EV], z[EV], w[EV], b[EV], dz[EV];
+        see(q, 0, v, x);
+        if constexpr (BWD) see(q, 1, v, d);
+        if constexpr (GATE) see(q, 1 + BWD, v, z);
+        weights(col(v), w);
+        if constexpr (GATE || !BWD) weights(cols + col(v), b);
+#pragma unroll
+        for (int e = 0; e < EV; ++e) {
+          const V n = mul(add(x[e], all<V>(-mean)), all<V>(rstd));
+          if constexpr (!BWD) {
+            x[e] = fma_(n, w[e], b[e]);
+            if constexpr (GATE) x[e] = mul(x[e], silu(z[e]));
+          } else {
+            V h = d[e];
+            if constexpr (GATE) {
+              const V zb = bounded(z[e]), sg = sigmoid(zb), zs = mul(zb, sg);
+              dz[e] = mul(mul(h, fma_(n, w[e], b[e])), fma_(zs, fma_(sg, all<V>(-1.f), all<V>(1.f)), sg));
+              h = mul(h, zs);
+            }
+            dw[v][e] = fma_(h, n, dw[v][e]);
+            db[v][e] = add(db[v][e], h);
+            x[e] = mul(all<V>(rstd), add(fma_(n, all<V>(-m2), mul(h, w[e])), all<V>(-m1)));
           }
-          dw[v][e] = fmaf(h, n, dw[v][e]);
-          db[v][e] += h;
-          x[e] = rstd * (fmaf(-n, m2, h * w[e]) - m1);
         }
+        Pk::store(static_cast<T*>(a.out) + r * cols + col(v), x);
+        if constexpr (BWD && GATE) Pk::store(static_cast<T*>(a.dz) + r * cols + col(v), dz);
       }
-      Pk::store(static_cast<T*>(a.out) + r * cols + col(v), x);
-      if constexpr (BWD && GATE) Pk::store(static_cast<T*>(a.dz) + r * cols + col(v), dz);
     }
   }
   if constexpr (BWD) {
@@ -419,9 +534,9 @@ __global__ void __launch_bounds__(BT, MINB) k_norm_row(const Args a) {
     for (int v = 0; v < VPL; ++v)
       if (col(v) < cols) {
 #pragma unroll
-        for (int e = 0; e < E; e += 4) {
-          *reinterpret_cast<float4*>(pw + col(v) + e) = make_float4(dw[v][e], dw[v][e + 1], dw[v][e + 2], dw[v][e + 3]);
-          *reinterpret_cast<float4*>(pb + col(v) + e) = make_float4(db[v][e], db[v][e + 1], db[v][e + 2], db[v][e + 3]);
+        for (int e = 0; e < EV; e += 2) {
+          *reinterpret_cast<float4*>(pw + col(v) + 2 * e) = make_float4(dw[v][e].x, dw[v][e].y, dw[v][e + 1].x, dw[v][e + 1].y);
+          *reinterpret_cast<float4*>(pb + col(v) + 2 * e) = make_float4(db[v][e].x, db[v][e].y, db[v][e + 1].x, db[v][e + 1].y);
         }
       }
   }
@@ -461,7 +576,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_wide(const Args a) {
         float h = to_f(dout[c]);
         const float w = a.w ? a.w[c] : 1.f;
         if (z) {
-          const float zv = to_f(z[c]), sg = sigmoid(zv);
+          const float zv = bounded(to_f(z[c])), sg = sigmoid(zv);
           put(static_cast<T*>(a.dz) + r * cols + c,
               h * fmaf(n, w, a.b ? a.b[c] : 0.f) * (sg * fmaf(zv, 1.f - sg, 1.f)));
           h *= zv * sg;
@@ -501,17 +616,18 @@ __global__ void __launch_bounds__(kThreads) k_norm_wide_cols(const Args a) {
   a.part[((int64_t)kParts + blockIdx.y) * cols + c] = db;
 }
 
-// dw and db from the partial sums: 32 columns a CTA, eight strands of parts
-// each, the strands added in order.
-__global__ void __launch_bounds__(kThreads) k_norm_sum(const float* __restrict__ part, int parts, int64_t cols,
+// dw and db from the partial sums: 32 columns a CTA, 32 strands of parts each,
+// the strands added in order.
+constexpr int kSumThreads = 1024, kStrands = kSumThreads / 32;
+__global__ void __launch_bounds__(kSumThreads) k_norm_sum(const float* __restrict__ part, int parts, int64_t cols,
                                                        float* dw, float* db) {
-  __shared__ double s[2][8][32];
+  __shared__ double s[2][kStrands][32];
   const int l = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + l;
   double p = 0., q = 0.;
   if (c < cols) {
 #pragma unroll 4
-    for (int i = g; i < parts; i += 8) {
+    for (int i = g; i < parts; i += kStrands) {
       p += part[i * cols + c];
       q += part[((int64_t)kParts + i) * cols + c];
     }
@@ -521,7 +637,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_sum(const float* __restrict__
   if (g < 2 && c < cols) {
     double t = 0.;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += s[g][i][l];
+    for (int i = 0; i < kStrands; ++i) t += s[g][i][l];
     if (g == 0 && dw) dw[c] = (float)t;
     if (g == 1 && db) db[c] = (float)t;
   }
@@ -546,12 +662,10 @@ cudaError_t launch_row(const Args& a, cudaStream_t st, int* parts) {
   const unsigned grid = (unsigned)(a.rows < most ? a.rows : most);
   *parts = (int)grid;
   const int threads = (int)((a.cols / 8 + 32 * VPL - 1) / (32 * VPL) * 32);
-  const size_t smem = (size_t)a.cols * (BWD && !a.z ? 4 : 8);  // at most 64 KB
   const auto kern = a.z ? k_norm_row<VPL, BT, MINB, BWD, true> : k_norm_row<VPL, BT, MINB, BWD, false>;
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
-    if (e != cudaSuccess) return e;
-  }
+  const size_t smem = a.z ? RowRing<VPL, BWD, true>::bytes(threads, a.cols) : RowRing<VPL, BWD, false>::bytes(threads, a.cols);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
   kern<<<grid, threads, smem, st>>>(a);
   return cudaGetLastError();
 }
@@ -666,6 +780,6 @@ extern "C" SSD_API ssd_status ssd_layer_norm_bwd(const ssd_norm_bwd_args* a, voi
     else k_norm_wide_cols<float><<<grid, kThreads, 0, st>>>(k);
     if (cudaGetLastError() != cudaSuccess) return SSD_ERR_CUDA;
   }
-  k_norm_sum<<<(unsigned)((a->cols + 31) / 32), kThreads, 0, st>>>(part, parts, a->cols, a->dweight, a->dbias);
+  k_norm_sum<<<(unsigned)((a->cols + 31) / 32), kSumThreads, 0, st>>>(part, parts, a->cols, a->dweight, a->dbias);
   return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }

@@ -85,6 +85,24 @@ def test_gate_far_out():
     assert torch.isfinite(y).all() and rel(y, ref) <= 2e-6 and not y[2].any()
 
 
+def test_gate_far_out_backward():
+    """A gate of -inf passes nothing: dz and the row's share of the rest are
+    zero; and no group without a row adds to the sums (eps = 0)."""
+    x, w, b, z, dy = make(3, 64, "f32", True, True, seed=9)
+    z[1] = -torch.inf
+    dx, dw, db, dz = ssd.layer_norm_bwd(x, w, b, dy, eps=0.0, z=z)
+    assert not dx[1].any() and not dz[1].any()
+    keep = [0, 2]
+    want = ssd.layer_norm_bwd(x[keep], w, b, dy[keep], eps=0.0, z=z[keep])
+    assert rel(dw, want[1]) <= 1e-6 and rel(db, want[2]) <= 1e-6
+    for cols in (1030, 4100):  # a CTA a row, and rows swept from memory
+        x, w, b, z, dy = make(3, cols, "bf16", True, True, seed=10)
+        z[1] = -torch.inf
+        assert not ssd.layer_norm(x, w, b, z=z)[1].any()
+        got = ssd.layer_norm_bwd(x, w, b, dy, z=z)
+        assert not got[0][1].any() and not got[3][1].any() and all(torch.isfinite(t).all() for t in got)
+
+
 def test_shapes_strides_and_places():
     x, w, b, z, dy = make(60, 64, "bf16", True, True, seed=5)
     y = ssd.layer_norm(x, w, b, z=z)

@@ -672,10 +672,9 @@ template <typename T, int NT>
 cudaError_t launch_grads_nt(const GradArgs& a, cudaStream_t stream) {
   constexpr int smem = GradTiles<T, NT>::kBytes;
   static_assert(smem <= 220 * 1024, "shared memory");
-  const cudaError_t e = cudaFuncSetAttribute(k_delta_grads<T, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  k_delta_grads<T, NT><<<(unsigned)(a.slots_n * a.G * a.nslices * a.splits), kGradThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  static std::atomic<uint64_t> seen{0};
+  return launch_kernel(k_delta_grads<T, NT>, seen, (unsigned)(a.slots_n * a.G * a.nslices * a.splits), kGradThreads, smem, smem,
+                       false, stream, a);
 }
 
 template <typename T>

@@ -26,6 +26,7 @@
 #pragma once
 
 #include "ssd_delta.cuh"
+#include "ssd_internal.h"
 
 namespace ssd {
 namespace delta {
@@ -375,11 +376,8 @@ cudaError_t launch_prep_nt(PrepArgs& a, int64_t chunks, cudaStream_t stream) {
   splits = splits < 1 ? 1 : splits > most ? most : splits;
   a.heads = (int)((a.hpg + splits - 1) / splits);
   a.splits = (int)((a.hpg + a.heads - 1) / a.heads);
-  const cudaError_t e =
-      cudaFuncSetAttribute(k_delta_prep<T, NT, FWD, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  k_delta_prep<T, NT, FWD, REV><<<(unsigned)(units * a.splits), kPrepThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  static std::atomic<uint64_t> seen{0};
+  return launch_kernel(k_delta_prep<T, NT, FWD, REV>, seen, (unsigned)(units * a.splits), kPrepThreads, smem, smem, false, stream, a);
 }
 
 template <typename T, bool FWD, bool REV>

@@ -122,7 +122,8 @@ template <typename T, int NT>
 cudaError_t launch_rwalk_nt(const WalkArgs& a, cudaStream_t stream) {
   constexpr int smem = Buffers<T, NT, true, 2>::kBytes;
   static_assert(smem <= 227 * 1024, "shared memory");
-  return launch_after(k_delta_rwalk<T, NT>, (unsigned)a.units, smem, a, stream);
+  static std::atomic<uint64_t> seen{0};
+  return launch_kernel(k_delta_rwalk<T, NT>, seen, (unsigned)a.units, kThreads, smem, smem, true, stream, a);
 }
 
 template <typename T>

@@ -548,25 +548,12 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(cons
     store_state<NT>(S, unit.sig.x, unit.sig.y, a.fin + (((int64_t)run.fin * a.H + h) * a.P + p0) * a.N, a.N, rows, lane);
 }
 
-// Launch a walk; its CTAs may start while the tiles' kernel ends.
-template <typename K, typename A>
-cudaError_t launch_after(K kern, unsigned grid, int smem, const A& args, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(grid), c.blockDim = dim3(kThreads), c.dynamicSmemBytes = smem, c.stream = stream;
-  cudaLaunchAttribute at = {};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &at, c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kern, args);
-}
-
 template <typename T, int NT, int MODE>
 cudaError_t launch_walk_nt(const WalkArgs& a, cudaStream_t stream) {
   constexpr int smem = Buffers<T, NT, MODE == kForward, MODE != kForward ? 0 : sizeof(T) == 4 ? 2 : 1>::kBytes;
   static_assert(smem <= 227 * 1024, "shared memory");
-  return launch_after(k_delta_walk<T, NT, MODE>, (unsigned)a.units, smem, a, stream);
+  static std::atomic<uint64_t> seen{0};
+  return launch_kernel(k_delta_walk<T, NT, MODE>, seen, (unsigned)a.units, kThreads, smem, smem, true, stream, a);
 }
 
 template <typename T, int MODE>

@@ -661,13 +661,17 @@ cudaError_t launch_row(const Args& a, cudaStream_t st, int* parts) {
   const int64_t most = MINB * kSMs;
   const unsigned grid = (unsigned)(a.rows < most ? a.rows : most);
   *parts = (int)grid;
-  const int threads = (int)((a.cols / 8 + 32 * VPL - 1) / (32 * VPL) * 32);
-  const auto kern = a.z ? k_norm_row<VPL, BT, MINB, BWD, true> : k_norm_row<VPL, BT, MINB, BWD, false>;
-  const size_t smem = a.z ? RowRing<VPL, BWD, true>::bytes(threads, a.cols) : RowRing<VPL, BWD, false>::bytes(threads, a.cols);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  kern<<<grid, threads, smem, st>>>(a);
-  return cudaGetLastError();
+  const unsigned threads = (unsigned)((a.cols / 8 + 32 * VPL - 1) / (32 * VPL) * 32);
+  constexpr int kMost = BT * VPL * 8;  // columns
+  static std::atomic<uint64_t> seen[2] = {};
+  if (a.z) {
+    using R = RowRing<VPL, BWD, true>;
+    return launch_kernel(k_norm_row<VPL, BT, MINB, BWD, true>, seen[1], grid, threads, R::bytes(threads, a.cols),
+                         R::bytes(BT, kMost), false, st, a);
+  }
+  using R = RowRing<VPL, BWD, false>;
+  return launch_kernel(k_norm_row<VPL, BT, MINB, BWD, false>, seen[0], grid, threads, R::bytes(threads, a.cols),
+                       R::bytes(BT, kMost), false, st, a);
 }
 
 // The group by the row's packs: part of a warp up to 64 packs (no barrier),

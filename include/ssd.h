@@ -532,8 +532,9 @@ typedef struct {
   float scale;                 /* of y; dstate^-1/2 is usual                     */
 } ssd_delta_args;
 
-/* Workspace bytes ssd_delta_fwd needs (sizes, dtype and the presence of
- * seq_idx only), or 0 if the sizes are invalid. */
+/* Workspace bytes ssd_delta_fwd needs (sizes, dtype, the presence of seq_idx
+ * and whether v lies on a 16-byte boundary only), or 0 if the sizes are
+ * invalid. */
 SSD_API size_t ssd_delta_fwd_workspace_size(const ssd_delta_args* args);
 
 /* Enqueue the forward on `stream`: two kernels, and one before them with
@@ -597,7 +598,8 @@ typedef struct {
   size_t workspace_bytes;
 } ssd_delta_bwd_args;
 
-/* Workspace bytes ssd_delta_bwd needs, or 0 if the sizes are invalid. */
+/* Workspace bytes ssd_delta_bwd needs (as above, with the presence of
+ * dfinal_states and the place of dy), or 0 if the sizes are invalid. */
 SSD_API size_t ssd_delta_bwd_workspace_size(const ssd_delta_bwd_args* args);
 
 SSD_API ssd_status ssd_delta_bwd(const ssd_delta_bwd_args* args, void* stream);

@@ -12,11 +12,14 @@ using namespace ssd::delta;
 namespace {
 
 struct Layout {
-  size_t runs, tokens, fwd, rev, e, d, s, ds, s_fin, max_y, max_e, max_d, max_s, max_ds, part, qdq, dvv, pi, total;
+  size_t runs, tokens, fwd, rev, e, d, s, ds, s_fin, max_y, max_e, max_d, max_s, max_ds, part, qdq, dvv, pi, v, dy, total;
   int nslices, splits, heads, pg;
 };
 
-Layout layout(const Shape& s, bool dfinal) {
+int64_t pitch_e(const Shape& s) { return (s.P + 3) / 4 * 4; }
+
+Layout layout(const Shape& s, const ssd_delta_bwd_args* b) {
+  const bool dfinal = b->dfinal_states != nullptr;
   Layout l;
   size_t at = runs_bytes(s);
   l.runs = 0;
@@ -38,8 +41,8 @@ Layout layout(const Shape& s, bool dfinal) {
   l.tokens = take(token_tiles_bytes(s));
   l.fwd = take((size_t)s.chunks * s.H * HeadTiles<0>::kStride);
   l.rev = take((size_t)s.chunks * s.H * RevTiles::kStride);
-  l.e = take(tokens * s.H * s.P * 4);
-  l.d = take(tokens * s.H * s.P * 4);
+  l.e = take(tokens * s.H * pitch_e(s) * 4);
+  l.d = take(tokens * s.H * pitch_e(s) * 4);
   l.s = take((size_t)s.slots * hpn * 4);
   l.ds = take((size_t)s.slots * hpn * 4);
   l.s_fin = take(dfinal ? (size_t)s.runs * hpn * 4 : 0);
@@ -49,6 +52,8 @@ Layout layout(const Shape& s, bool dfinal) {
   l.qdq = take((size_t)l.nslices * tokens * s.H * 4);
   l.dvv = take(tokens * s.H * 4);
   l.pi = take((size_t)l.nslices * s.slots * s.H * 4);
+  l.v = take(pad_bytes(s, b->fwd.v));
+  l.dy = take(pad_bytes(s, b->dy));
   l.total = at;
   return l;
 }
@@ -64,32 +69,43 @@ cudaError_t run_all(const ssd_delta_bwd_args* b, const Shape& s, const Layout& l
   p.scale = s.scale, p.q = a->q, p.k = a->k, p.g = a->g, p.beta = a->beta, p.chunks = runs.chunks;
   p.tokens = ws + l.tokens, p.fwd = ws + l.fwd, p.rev = ws + l.rev;
   p.vec = s.N * esz % 16 == 0 && aligned(a->q, 16) && aligned(a->k, 16);
-  cudaError_t e = launch_prep<T, true, true>(p, s.chunks, st);
+  cudaError_t e = cudaSuccess;
+  const int64_t rows = s.b * s.L * s.H, pv = pitch_of(s);
+  const void* v = a->v;
+  const void* dy = b->dy;
+  if (pad_bytes(s, v)) {
+    v = ws + l.v;
+    if ((e = launch_pad<T>(a->v, ws + l.v, rows, s.P, pv, st)) != cudaSuccess) return e;
+  }
+  if (pad_bytes(s, dy)) {
+    dy = ws + l.dy;
+    if ((e = launch_pad<T>(b->dy, ws + l.dy, rows, s.P, pv, st)) != cudaSuccess) return e;
+  }
+  e = launch_prep<T, true, true>(p, s.chunks, st);
   if (e != cudaSuccess) return e;
   WalkArgs w = {};
+  w.pv = pv, w.pe = pitch_e(s);
   w.L = s.L, w.H = s.H, w.G = s.G, w.P = s.P, w.N = s.N, w.hpg = p.hpg;
   w.slices = (int)((s.P + kP - 1) / kP), w.units = s.runs * s.H * w.slices;
-  w.tokens = p.tokens, w.heads = p.fwd, w.v = a->v, w.s0 = a->initial_states, w.runs = runs.runs;
-  w.pg = l.pg, w.out = at(l.e), w.out_vec = s.P % 4 == 0, w.max_out = at(l.max_e);
+  w.tokens = p.tokens, w.heads = p.fwd, w.v = v, w.s0 = a->initial_states, w.runs = runs.runs;
+  w.pg = l.pg, w.out = at(l.e), w.max_out = at(l.max_e);
   w.check = at(l.s), w.max_check = at(l.max_s), w.fin = b->dfinal_states ? at(l.s_fin) : nullptr;
-  w.v_vec = s.P * esz % 16 == 0 && aligned(a->v, 16);
   if ((e = launch_walk<T, kStates>(w, st)) != cudaSuccess) return e;
-  w.heads = p.rev, w.v = b->dy, w.s0 = b->dfinal_states, w.out = b->dv, w.out_f = at(l.d);
+  w.heads = p.rev, w.v = dy, w.s0 = b->dfinal_states, w.out = b->dv, w.out_f = at(l.d);
   w.max_v = at(l.max_y), w.max_out = at(l.max_d), w.check = at(l.ds), w.max_check = at(l.max_ds);
   w.fin = b->dinitial_states;
-  w.v_vec = s.P * esz % 16 == 0 && aligned(b->dy, 16), w.out_vec = s.P * esz % 16 == 0 && aligned(b->dv, 16);
+  w.out_vec = s.P * esz % 16 == 0 && aligned(b->dv, 16);
   if ((e = launch_rwalk<T>(w, st)) != cudaSuccess) return e;
   GradArgs g = {};
   g.L = s.L, g.H = s.H, g.G = s.G, g.P = s.P, g.N = s.N, g.hpg = p.hpg;
   g.per_row = (int)((s.L + kCheck - 1) / kCheck), g.splits = l.splits, g.heads = l.heads, g.nslices = l.nslices;
-  g.pg = l.pg, g.scale = s.scale, g.tokens = p.tokens, g.head = p.rev, g.v = a->v, g.dy = b->dy;
+  g.pg = l.pg, g.scale = s.scale, g.tokens = p.tokens, g.head = p.rev, g.v = v, g.dy = dy, g.pv = pv, g.pe = w.pe;
   g.e = at(l.e), g.d = at(l.d), g.s = at(l.s), g.ds = at(l.ds), g.s_fin = b->dfinal_states ? at(l.s_fin) : nullptr;
   g.max_y = at(l.max_y), g.max_e = at(l.max_e), g.max_d = at(l.max_d), g.max_s = at(l.max_s), g.max_ds = at(l.max_ds);
   g.initial = a->initial_states != nullptr;
   g.slots = runs.slots, g.slots_n = s.slots, g.dq = b->dq, g.dk = b->dk;
   g.part = at(l.part), g.part_size = s.b * s.L * s.G * s.N;
   g.qdq = at(l.qdq), g.part_stride = s.b * s.L * s.H, g.dvv = at(l.dvv), g.pi = at(l.pi), g.dbeta = b->dbeta;
-  g.vec = s.P % 4 == 0 && aligned(a->v, 4 * esz) && aligned(b->dy, 4 * esz);
   g.pair = s.N % 2 == 0 && aligned(b->dq, 2 * esz) && aligned(b->dk, 2 * esz);
   return launch_grads<T>(g, b->dg, st);
 }
@@ -99,7 +115,7 @@ cudaError_t run_all(const ssd_delta_bwd_args* b, const Shape& s, const Layout& l
 extern "C" SSD_API size_t ssd_delta_bwd_workspace_size(const ssd_delta_bwd_args* b) {
   Shape s;
   if (!b || resolve(&b->fwd, &s) != SSD_OK) return 0;
-  return layout(s, b->dfinal_states != nullptr).total;
+  return layout(s, b).total;
 }
 
 extern "C" SSD_API ssd_status ssd_delta_bwd(const ssd_delta_bwd_args* b, void* stream) {
@@ -110,7 +126,7 @@ extern "C" SSD_API ssd_status ssd_delta_bwd(const ssd_delta_bwd_args* b, void* s
   if (c != SSD_OK) return c;
   if (!a->q || !a->k || !a->v || !a->g || !a->beta || !b->dy || !b->dq || !b->dk || !b->dv || !b->dg || !b->dbeta)
     return SSD_ERR_INVALID_ARG;
-  const Layout l = layout(s, b->dfinal_states != nullptr);
+  const Layout l = layout(s, b);
   if ((double)s.slots * s.G * l.nslices * l.splits >= 2147483647.0) return SSD_ERR_UNSUPPORTED;
   if (!b->workspace || b->workspace_bytes < l.total) return SSD_ERR_WORKSPACE;
   if (!aligned(b->workspace, kWsAlign)) return SSD_ERR_INVALID_ARG;

@@ -59,7 +59,7 @@ struct GradArgs {
   float* pi;            // [nslice][slot][H]
   float* dbeta;
   int64_t slots_n;
-  int vec;              // rows of v and dy can be read by fours
+  int64_t pv, pe;       // row pitches of v and dy, and of e and d: multiples of four
   bool initial;         // there are initial states
   int pair;             // dq and dk can be written by twos
 };
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
   // A piece is 64 columns of headdim of one head.  What the next piece needs is
   // copied while this one is worked on: decays and largest magnitudes, E, D, V
   // and dY, and, where this piece's operands have been used up, the states.
-  const bool v4 = a.P % 4 == 0, n4 = a.N % 4 == 0;
+  const bool n4 = a.N % 4 == 0;
   const auto copy_small = [&](int64_t h, int p0) {
     if (h >= h1) return;
     const int t = threadIdx.x;
@@ -291,11 +291,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
       for (int x = 0; x < 64 * 16 / kGradThreads; ++x) {
         const int t = (threadIdx.x >> 4) + (kGradThreads / 16) * x, p = (threadIdx.x & 15) * 4;
         const int left = t < sl.n ? (int)(a.P - p0 - p) : 0;
-        const int64_t o = (((int64_t)sl.tok + t) * a.H + h) * a.P + p0 + p;
-        copy4(sm + G::kRawE + (t * 64 + p) * 4, a.e, o, left, v4);
-        copy4(sm + G::kRawD + (t * 64 + p) * 4, a.d, o, left, v4);
-        copy4(sm + G::kRawV + (t * 64 + p) * (int)sizeof(T), static_cast<const T*>(a.v), o, left, a.vec);
-        copy4(sm + G::kRawY + (t * 64 + p) * (int)sizeof(T), static_cast<const T*>(a.dy), o, left, a.vec);
+        const int64_t th = ((int64_t)sl.tok + t) * a.H + h, oe = th * a.pe + p0 + p, ov = th * a.pv + p0 + p;
+        copy4(sm + G::kRawE + (t * 64 + p) * 4, a.e, oe, left, true);
+        copy4(sm + G::kRawD + (t * 64 + p) * 4, a.d, oe, left, true);
+        copy4(sm + G::kRawV + (t * 64 + p) * (int)sizeof(T), static_cast<const T*>(a.v), ov, left, true);
+        copy4(sm + G::kRawY + (t * 64 + p) * (int)sizeof(T), static_cast<const T*>(a.dy), ov, left, true);
       }
     }
   };
@@ -390,11 +390,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
           get4(reinterpret_cast<const T*>(sm + G::kRawV) + t * 64 + p, u4);
         } else {
           const int left = t < sl.n ? (int)(a.P - p0 - p) : 0;
-          const int64_t o = (((int64_t)sl.tok + t) * a.H + h) * a.P + p0 + p;
-          get4(a.e + o, left, v4, e4);
-          get4(a.d + o, left, v4, d4);
-          get4(static_cast<const T*>(a.dy) + o, left, a.vec, y4);
-          get4(static_cast<const T*>(a.v) + o, left, a.vec, u4);
+          const int64_t th = ((int64_t)sl.tok + t) * a.H + h, oe = th * a.pe + p0 + p, ov = th * a.pv + p0 + p;
+          get4(a.e + oe, left, true, e4);
+          get4(a.d + oe, left, true, d4);
+          get4(static_cast<const T*>(a.dy) + ov, left, true, y4);
+          get4(static_cast<const T*>(a.v) + ov, left, true, u4);
         }
         float de = 0.f, dv = 0.f;
 #pragma unroll

@@ -24,12 +24,12 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_rwalk(con
   const Run run = a.runs ? a.runs[ri] : row_run(ri, a.L);
   const int nc = (run.len + kC - 1) / kC;
   const int p_cta = slice * kP, p0 = p_cta + 16 * warp;
-  const int cols = (int)(a.P - p_cta < kP ? a.P - p_cta : kP);
+  const int cols = (int)(a.pv - p_cta < kP ? a.pv - p_cta : kP);
   const int rows = a.P - p0 < 16 ? (int)(a.P - p0) : 16;
-  const int64_t vstride = a.H * a.P, tstride = a.G * X::kBytes, hstride = a.H * Hd::kStride;
+  const int64_t vstride = a.H * a.pv, tstride = a.G * X::kBytes, hstride = a.H * Hd::kStride;
   const char* tok = a.tokens + (run.chunk * a.G + h / a.hpg) * X::kBytes;
   const char* head = a.heads + (run.chunk * a.H + h) * Hd::kStride;
-  const T* v = static_cast<const T*>(a.v) + (run.tok * a.H + h) * a.P + p_cta;
+  const T* v = static_cast<const T*>(a.v) + (run.tok * a.H + h) * a.pv + p_cta;
   float S[NT / 8][4];
   if (a.s0 && run.fin >= 0) {
     load_state<NT>(S, a.s0 + (((int64_t)run.fin * a.H + h) * a.P + p0) * a.N, a.N, rows, lane);
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_rwalk(con
   const auto fetch = [&](int j) {
     const int n = run.len - j * kC;
     fetch_chunk<T, NT, true, 2>(tok + j * tstride, head + j * hstride, v + (int64_t)j * kC * vstride, vstride, n, cols,
-                                a.v_vec, sm + (j & 1) * B::kBuf);
+                                sm + (j & 1) * B::kBuf);
   };
   if (nc > 0) fetch(nc - 1);
   for (int j = nc - 1; j >= 0; --j) {
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_rwalk(con
     lower_mma_t<true>(d, hi, lo, tt, lane);
     // D: at most 32 products of two operands below 2^15 and a power of two
     const int n = run.len - j * kC < kC ? run.len - j * kC : kC;
-    const int64_t row0 = ((run.tok + (int64_t)j * kC) * a.H + h) * a.P + p0;
+    const int64_t th = (run.tok + (int64_t)j * kC) * a.H + h, row0 = th * a.P + p0, rowe = th * a.pe + p0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       d[i][0] *= iv.x, d[i][1] *= iv.x, d[i][2] *= iv.y, d[i][3] *= iv.y;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_rwalk(con
       const float m = warp_absmax(tile_max(d));
       if (lane == 0) a.max_out[at] = m;
     }
-    store_tile<float>(d, stage, a.out_f + row0, a.H * a.P, n, rows, a.P % 4 == 0, lane);
+    store_tile<float>(d, stage, a.out_f + rowe, a.H * a.pe, n, (rows + 3) & ~3, true, lane);
     store_tile<T>(e, stage, static_cast<T*>(a.out) + row0, a.H * a.P, n, rows, a.out_vec, lane);
     // dS' = exp(cs_C) dS + (scale exp(cs) dY) q - (beta exp(cs) D) k
     const float yb = ymax * f.qcm;

@@ -35,7 +35,7 @@ struct WalkArgs {
   int64_t units;       // (run, head, slice)
   const char* tokens;  // [chunk][group] TokenTiles
   const char* heads;   // [chunk][head] HeadTiles
-  const void* v;       // forward: v; reverse: dy
+  const void* v;       // forward: v; reverse: dy; rows of `pv` elements on 16-byte boundaries
   const float* s0;     // state a run starts from (reverse: gradient of the final state), or null
   const Run* runs;     // or null: a run for each row
   void* out;           // forward: y; state walk: E (fp32); reverse: dv
@@ -46,7 +46,9 @@ struct WalkArgs {
   float* max_check;    // for the kernel that turns them into operands
   int pg;              // sixteens of headdim
   float* fin;          // final state (forward) or gradient of the initial state (reverse), or null
-  int v_vec, out_vec;  // rows start on 16-byte boundaries
+  int64_t pv;          // row pitch of v
+  int64_t pe;          // row pitch of E and D: headdim rounded up to fours
+  int out_vec;         // rows of y or dv start on 16-byte boundaries
 };
 
 // A chunk's tiles in shared memory, two buffers.
@@ -63,11 +65,40 @@ struct Buffers {
   static_assert(kBuf % 16 == 0, "16-byte copies");
 };
 
+// Rows of v or dy that do not start on 16-byte boundaries are copied, by a
+// kernel before the walk, to rows that do, with zeros behind headdim: reading
+// them element by element in the walk, between two chunks, took it from 2.0 to
+// 4.1 us a chunk.
+template <typename T>
+__global__ void __launch_bounds__(256) k_delta_pad(const T* __restrict__ from, T* __restrict__ to, int64_t rows, int64_t P,
+                                                   int64_t pitch) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * pitch; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / pitch, c = i - r * pitch;
+    to[i] = c < P ? from[r * P + c] : from_f<T>(0.f);
+  }
+}
+template <typename T>
+cudaError_t launch_pad(const void* from, void* to, int64_t rows, int64_t P, int64_t pitch, cudaStream_t stream) {
+  const int64_t need = (rows * pitch + 255) / 256;
+  k_delta_pad<T><<<(unsigned)(need < 8 * 148 ? need : 8 * 148), 256, 0, stream>>>(static_cast<const T*>(from),
+                                                                                   static_cast<T*>(to), rows, P, pitch);
+  return cudaGetLastError();
+}
+// Row pitch of v as the walks read it, and bytes of its padded copy (0: it is read where it lies).
+inline int64_t pitch_of(const Shape& s) {
+  const int64_t e = s.bf16 ? 8 : 4;
+  return (s.P + e - 1) / e * e;
+}
+inline size_t pad_bytes(const Shape& s, const void* v) {
+  const size_t esz = s.bf16 ? 2 : 4;
+  return s.P == pitch_of(s) && aligned(v, 16) ? 0 : (size_t)s.b * s.L * s.H * pitch_of(s) * esz;
+}
+
 // Enqueue the copies of one chunk: the group's tiles, the head's, and its rows
 // of V (n of them exist, `cols` columns; the rest become zeros).
 template <typename T, int NT, bool Q, int MTERMS>
 __device__ __forceinline__ void fetch_chunk(const char* tok, const char* head, const T* v, int64_t vstride, int n, int cols,
-                                            bool vec, char* buf) {
+                                            char* buf) {
   using B = Buffers<T, NT, Q, MTERMS>;
   const uint32_t d = sm100::smem_u32(buf);
 #pragma unroll
@@ -88,13 +119,7 @@ __device__ __forceinline__ void fetch_chunk(const char* tok, const char* head, c
     const int row = row0 + x * kStep;
     const bool ok = row < n && c < cols;
     const uint32_t o = B::kV + (row * B::kVP + c) * (int)sizeof(T);
-    if (vec) {
-      cp_async16(d + o, ok ? v + row * vstride + c : v, ok);
-    } else {
-      T* dst = reinterpret_cast<T*>(buf + o);
-#pragma unroll 1
-      for (int e = 0; e < E; ++e) dst[e] = ok && c + e < cols ? v[row * vstride + c + e] : from_f<T>(0.f);
-    }
+    cp_async16(d + o, ok ? v + row * vstride + c : v, ok);
   }
   cp_async_commit();
 }
@@ -467,12 +492,12 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(cons
   const Run run = a.runs ? a.runs[ri] : row_run(ri, a.L);
   const int nc = (run.len + kC - 1) / kC;
   const int p_cta = slice * kP, p0 = p_cta + 16 * warp;
-  const int cols = (int)(a.P - p_cta < kP ? a.P - p_cta : kP);
+  const int cols = (int)(a.pv - p_cta < kP ? a.pv - p_cta : kP);
   const int rows = a.P - p0 < 16 ? (int)(a.P - p0) : 16;  // may be negative: nothing is read or written
-  const int64_t vstride = a.H * a.P, tstride = a.G * X::kBytes, hstride = a.H * Hd::kStride;
+  const int64_t vstride = a.H * a.pv, tstride = a.G * X::kBytes, hstride = a.H * Hd::kStride;
   const char* tok = a.tokens + (run.chunk * a.G + h / a.hpg) * X::kBytes;
   const char* head = a.heads + (run.chunk * a.H + h) * Hd::kStride;
-  const T* v = static_cast<const T*>(a.v) + (run.tok * a.H + h) * a.P + p_cta;
+  const T* v = static_cast<const T*>(a.v) + (run.tok * a.H + h) * a.pv + p_cta;
   float S[NT / 8][4];
   if (a.s0 && run.h0 >= 0) {
     load_state<NT>(S, a.s0 + (((int64_t)run.h0 * a.H + h) * a.P + p0) * a.N, a.N, rows, lane);
@@ -489,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(cons
   const auto fetch = [&](int j) {
     const int n = run.len - j * kC;
     fetch_chunk<T, NT, kY, kMTerms>(tok + j * tstride, head + j * hstride, v + (int64_t)j * kC * vstride, vstride, n, cols,
-                                    a.v_vec, sm + (j & 1) * B::kBuf);
+                                    sm + (j & 1) * B::kBuf);
   };
   if (nc > 0) fetch(0);
   for (int j = 0; j < nc; ++j) {
@@ -522,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(cons
     scale_tile(e, f.tau, make_float2(1.f, 1.f), lane);
     iv.x *= f.norm, iv.y *= f.norm;
     const int n = run.len - j * kC < kC ? run.len - j * kC : kC;
-    const int64_t row0 = ((run.tok + (int64_t)j * kC) * a.H + h) * a.P + p0;
+    const int64_t th = (run.tok + (int64_t)j * kC) * a.H + h, row0 = th * a.P + p0, rowe = th * a.pe + p0;
     if constexpr (kY) {
       as_operand<kTerms == 2>(e, hi, lo);
       scale_tile(y, f.qc, unit.sig, lane);
@@ -533,7 +558,8 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(cons
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[i][0] = e[i][0] * iv.x, y[i][1] = e[i][1] * iv.x, y[i][2] = e[i][2] * iv.y, y[i][3] = e[i][3] * iv.y;
-      store_tile<float>(y, stage, static_cast<float*>(a.out) + row0, a.H * a.P, n, rows, a.out_vec, lane);
+      // (zeros in the columns from headdim to the pitch)
+      store_tile<float>(y, stage, static_cast<float*>(a.out) + rowe, a.H * a.pe, n, (rows + 3) & ~3, true, lane);
       const float m = warp_absmax(32768.f * fmaxf(iv.x, iv.y));
       if (lane == 0) a.max_out[((run.chunk + j) * a.H + h) * a.pg + p0 / 16] = m;
     }

@@ -27,7 +27,7 @@ namespace {
 constexpr int kSMs = 148;
 constexpr int kThreads = 256;     // CTA of the kernels whose rows share one
 constexpr int kMostThreads = 512;  // CTA of one row, as many as it needs
-constexpr int kParts = 3 * kSMs;  // most CTAs of the backward, each with its partial sums
+constexpr int kParts = 3 * kSMs;  // most CTAs of the backward whose rows do not each take a CTA
 
 struct Args {
   int64_t rows, cols;
@@ -39,7 +39,7 @@ struct Args {
   const void* dout;
   void* out;    // forward: y; backward: dx
   void* dz;
-  float* part;  // backward: [2][kParts][cols] partial sums of dw, db, or null
+  float* part;  // backward: [2][CTAs][cols] partial sums of dw, db, or null
   float* stat;  // wide rows: [rows][2] mean, rstd
 };
 
@@ -92,6 +92,28 @@ struct Pack<__nv_bfloat16, 8> {
       u[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+template <>
+struct Pack<float, 2> {
+  using V = float2;
+  float2 r;
+  __device__ __forceinline__ void load(const float* p) { r = __ldcs(reinterpret_cast<const float2*>(p)); }
+  __device__ __forceinline__ void get(float2 (&f)[1]) const { f[0] = r; }
+  __device__ __forceinline__ void zero() { r = make_float2(0.f, 0.f); }
+  static __device__ __forceinline__ void store(float* p, const float2 (&f)[1]) { *reinterpret_cast<float2*>(p) = f[0]; }
+};
+template <>
+struct Pack<__nv_bfloat16, 2> {
+  using V = float2;
+  uint32_t r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = __ldcs(reinterpret_cast<const uint32_t*>(p)); }
+  __device__ __forceinline__ void get(float2 (&f)[1]) const {
+    f[0] = make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+  }
+  __device__ __forceinline__ void zero() { r = 0; }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float2 (&f)[1]) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __float22bfloat162_rn(f[0]);
   }
 };
 template <>
@@ -292,7 +314,7 @@ __global__ void __launch_bounds__(BT, MINB) k_norm(const Args a) {
     if (!a.part) return;
     // the CTA's groups added in order, one set of partial sums a CTA
     float* pw = a.part + blockIdx.x * cols;
-    float* pb = pw + (int64_t)kParts * cols;
+    float* pb = pw + (int64_t)gridDim.x * cols;
     const auto at = [](const V (&x)[EV], int e) { return reinterpret_cast<const float*>(&x)[e]; };
     if constexpr (GC == 1) {
 #pragma unroll
@@ -529,7 +551,7 @@ __global__ void __launch_bounds__(BT, MINB) k_norm_row(const Args a) {
   if constexpr (BWD) {
     if (!a.part) return;
     float* pw = a.part + (int64_t)blockIdx.x * cols;
-    float* pb = pw + (int64_t)kParts * cols;
+    float* pb = pw + (int64_t)gridDim.x * cols;
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
       if (col(v) < cols) {
@@ -613,7 +635,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_wide_cols(const Args a) {
     db += h;
   }
   a.part[blockIdx.y * cols + c] = dw;
-  a.part[((int64_t)kParts + blockIdx.y) * cols + c] = db;
+  a.part[((int64_t)gridDim.y + blockIdx.y) * cols + c] = db;
 }
 
 // dw and db from the partial sums: 32 columns a CTA, 32 strands of parts each,
@@ -629,7 +651,7 @@ __global__ void __launch_bounds__(kSumThreads) k_norm_sum(const float* __restric
 #pragma unroll 4
     for (int i = g; i < parts; i += kStrands) {
       p += part[i * cols + c];
-      q += part[((int64_t)kParts + i) * cols + c];
+      q += part[((int64_t)parts + i) * cols + c];
     }
   }
   s[0][g][l] = p, s[1][g][l] = q;
@@ -643,13 +665,21 @@ __global__ void __launch_bounds__(kSumThreads) k_norm_sum(const float* __restric
   }
 }
 
-// MINB CTAs an SM, which the kernel's registers allow, and one grid of them.
-// `threads`: of a CTA that takes one row; else GT threads take one.
+// CTAs of a grid with `threads` an SM (at most 16 an SM).
+int64_t ctas(int per_sm, int threads) {
+  const int n = per_sm / threads;
+  return (int64_t)kSMs * (n < 1 ? 1 : n > 16 ? 16 : n);
+}
+constexpr int kRowParts = 16384;  // CTAs of an SM times columns, where a row takes a CTA, are at most this
+
+// One grid of the CTAs that fit: the kernel's registers allow MINB CTAs of BT
+// threads an SM, or more of fewer.  `threads`: of a CTA that takes one row;
+// else GT threads take one.
 template <typename T, int E, int GT, int VPL, int BT, int MINB, bool BWD>
 cudaError_t launch(const Args& a, cudaStream_t st, int* parts, int threads = kThreads) {
   constexpr int GC = GT > 32 ? 1 : kThreads / GT;
-  const int64_t need = (a.rows + GC - 1) / GC, most = MINB * kSMs;
-  static_assert(!BWD || MINB * kSMs <= kParts, "partial sums");
+  const int64_t need = (a.rows + GC - 1) / GC, most = ctas(MINB * BT, threads);
+  static_assert(!BWD || (GT > 32 ? MINB * BT * E * VPL <= kRowParts : MINB * kSMs <= kParts), "partial sums");
   const unsigned grid = (unsigned)(need < most ? need : most);
   *parts = (int)grid;
   if (a.z) k_norm<T, E, GT, VPL, BT, MINB, BWD, true><<<grid, threads, 0, st>>>(a);
@@ -658,10 +688,11 @@ cudaError_t launch(const Args& a, cudaStream_t st, int* parts, int threads = kTh
 }
 template <int VPL, int BT, int MINB, bool BWD>
 cudaError_t launch_row(const Args& a, cudaStream_t st, int* parts) {
-  const int64_t most = MINB * kSMs;
+  const unsigned threads = (unsigned)((a.cols / 8 + 32 * VPL - 1) / (32 * VPL) * 32);
+  const int64_t most = ctas(MINB * BT, (int)threads);
+  static_assert(!BWD || MINB * BT * 8 * VPL <= kRowParts, "partial sums");
   const unsigned grid = (unsigned)(a.rows < most ? a.rows : most);
   *parts = (int)grid;
-  const unsigned threads = (unsigned)((a.cols / 8 + 32 * VPL - 1) / (32 * VPL) * 32);
   constexpr int kMost = BT * VPL * 8;  // columns
   static std::atomic<uint64_t> seen[2] = {};
   if (a.z) {
@@ -674,15 +705,33 @@ cudaError_t launch_row(const Args& a, cudaStream_t st, int* parts) {
                        R::bytes(BT, kMost), false, st, a);
 }
 
+// Rows that 16-byte packs do not divide, in pairs or single elements: half a
+// row to an eighth of the loads' width.
+template <typename T, int E, bool BWD>
+cudaError_t launch_narrow(const Args& a, cudaStream_t st, int* parts, bool* wide) {
+  constexpr int kB = BWD ? 2 : 4;
+  const int64_t n = a.cols / E;
+  const auto warps = [](int64_t n) { return (int)((n + 31) / 32 * 32); };
+  if (n <= 8) return launch<T, E, 8, 1, 256, kB, BWD>(a, st, parts);
+  if (n <= 32) return launch<T, E, 32, 1, 256, kB, BWD>(a, st, parts);
+  if (n <= 64) return launch<T, E, 32, 2, 256, kB, BWD>(a, st, parts);
+  if (n <= 160) return launch<T, E, 32, 5, 256, BWD ? (E == 1 ? 3 : 2) : (E == 1 ? 4 : 3), BWD>(a, st, parts);
+  if (n <= 1024) return launch<T, E, 64, 4, 256, kB, BWD>(a, st, parts, warps((n + 3) / 4));
+  if (n <= 4096) return launch<T, E, 64, 8, 512, BWD || E == 2 ? 1 : 2, BWD>(a, st, parts, warps((n + 7) / 8));
+  *wide = true;
+  return cudaSuccess;
+}
+
 // The group by the row's packs: part of a warp up to 64 packs (no barrier),
 // else a CTA of as many threads as the row needs with one or two packs each.
+// `vec`: elements to which every row is aligned (E, 2 or 1).
 template <typename T, bool BWD>
-cudaError_t launch_rows(const Args& a, bool vec, cudaStream_t st, int* parts, bool* wide) {
+cudaError_t launch_rows(const Args& a, int vec, cudaStream_t st, int* parts, bool* wide) {
   constexpr int E = 16 / (int)sizeof(T), kB = BWD ? 2 : 4;
   *wide = false;
   const auto warps = [](int64_t n) { return (int)((n + 31) / 32 * 32); };
-  if (vec) {
-    const int64_t n = a.cols / E;
+  const int64_t n = a.cols / E;
+  if (vec == E && n <= 1024) {
     if (n <= 4) return launch<T, E, 4, 1, 256, kB, BWD>(a, st, parts);
     if (n <= 8) return launch<T, E, 8, 1, 256, kB, BWD>(a, st, parts);
     if (n <= 16) return launch<T, E, 16, 1, 256, kB, BWD>(a, st, parts);
@@ -691,17 +740,16 @@ cudaError_t launch_rows(const Args& a, bool vec, cudaStream_t st, int* parts, bo
     if constexpr (sizeof(T) == 2) {
       if (n <= 256) return launch_row<1, 256, BWD ? 3 : 4, BWD>(a, st, parts);
       if (n <= 640) return launch_row<2, 320, BWD ? 2 : 3, BWD>(a, st, parts);
-      if (n <= 1024) return launch_row<2, 512, 1, BWD>(a, st, parts);
+      return launch_row<2, 512, 1, BWD>(a, st, parts);
     } else {
       if (n <= 256) return launch<T, E, 64, 1, 256, kB, BWD>(a, st, parts, warps(n));
-      if (n <= 1024) return launch<T, E, 64, 2, 512, 1, BWD>(a, st, parts, warps((n + 1) / 2));
+      return launch<T, E, 64, 2, 512, 1, BWD>(a, st, parts, warps((n + 1) / 2));
     }
-  } else {
-    if (a.cols <= 8) return launch<T, 1, 8, 1, 256, kB, BWD>(a, st, parts);
-    if (a.cols <= 32) return launch<T, 1, 32, 1, 256, kB, BWD>(a, st, parts);
-    if (a.cols <= 160) return launch<T, 1, 32, 5, 256, BWD ? 3 : 4, BWD>(a, st, parts);
-    if (a.cols <= 1024) return launch<T, 1, 64, 4, 256, kB, BWD>(a, st, parts, warps((a.cols + 3) / 4));
-    if (a.cols <= 4096) return launch<T, 1, 64, 8, 512, 1, BWD>(a, st, parts, warps((a.cols + 7) / 8));
+  }
+  if (vec != E) {
+    const cudaError_t e =
+        vec == 2 ? launch_narrow<T, 2, BWD>(a, st, parts, wide) : launch_narrow<T, 1, BWD>(a, st, parts, wide);
+    if (!*wide) return e;
   }
   *wide = true;
   const unsigned grid = (unsigned)(a.rows < 4 * kSMs ? a.rows : 4 * kSMs);
@@ -717,9 +765,12 @@ ssd_status check(int64_t rows, int64_t cols, ssd_dtype dtype, float eps) {
   return SSD_OK;
 }
 
-size_t bwd_workspace(int64_t rows, int64_t cols) {
-  return align_up((size_t)2 * kParts * (size_t)cols * 4, kWsAlign) + align_up((size_t)rows * 8, kWsAlign);
+// Partial sums, then the statistics of rows that are swept from memory.
+size_t part_bytes(int64_t cols) {
+  const size_t a = (size_t)kParts * (size_t)cols, b = (size_t)kSMs * kRowParts;
+  return align_up(2 * (a > b ? a : b) * 4, kWsAlign);
 }
+size_t bwd_workspace(int64_t rows, int64_t cols) { return part_bytes(cols) + align_up((size_t)rows * 8, kWsAlign); }
 
 }  // namespace
 }  // namespace ssd
@@ -736,7 +787,10 @@ extern "C" SSD_API ssd_status ssd_layer_norm(const ssd_norm_args* a, void* strea
   Args k = {};
   k.rows = a->rows, k.cols = a->cols, k.eps = a->eps;
   k.x = a->x, k.w = a->weight, k.b = a->bias, k.z = a->z, k.out = a->out;
-  const bool vec = a->cols * esz % 16 == 0 && aligned(a->x, 16) && aligned(a->z, 16) && aligned(a->out, 16);
+  const auto all_at = [&](size_t n) {
+    return a->cols * esz % n == 0 && aligned(a->x, n) && aligned(a->z, n) && aligned(a->out, n);
+  };
+  const int vec = all_at(16) ? (int)(16 / esz) : all_at(2 * esz) ? 2 : 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int parts;
   bool wide;
@@ -765,10 +819,13 @@ extern "C" SSD_API ssd_status ssd_layer_norm_bwd(const ssd_norm_bwd_args* a, voi
   float* part = static_cast<float*>(a->workspace);
   const bool sums = a->dweight || a->dbias;
   k.part = sums ? part : nullptr;
-  k.stat = reinterpret_cast<float*>(static_cast<char*>(a->workspace) +
-                                    align_up((size_t)2 * kParts * (size_t)a->cols * 4, kWsAlign));
-  bool vec = a->cols * esz % 16 == 0;
-  for (const void* p : {a->x, a->dout, (const void*)a->dx, a->z, (const void*)a->dz}) vec = vec && aligned(p, 16);
+  k.stat = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + part_bytes(a->cols));
+  const auto all_at = [&](size_t n) {
+    bool is = a->cols * esz % n == 0;
+    for (const void* p : {a->x, a->dout, (const void*)a->dx, a->z, (const void*)a->dz}) is = is && aligned(p, n);
+    return is;
+  };
+  const int vec = all_at(16) ? (int)(16 / esz) : all_at(2 * esz) ? 2 : 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int parts = 0;
   bool wide = false;

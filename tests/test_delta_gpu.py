@@ -387,3 +387,111 @@ def test_block_prefill_equals_decode_and_trains():
     norm(yr, wr, bias, 1e-5, zr).backward(dout.double())
     for got, want in ((xin, xr), (gl, gr), (bl, br), (zl, zr), (wl, wr)):
         assert rel(got.grad, want.grad) <= 1e-4, rel(got.grad, want.grad)  # as above, through the norm
+
+
+# ------------------------------------------------------------------ the far ends
+def test_offsets_past_32_bits():
+    """66000 tokens of 512 heads: v, y, the tiles, E, D and the checkpointed
+    states pass 2^31 elements.  The last group's heads do not depend on the
+    others, so a call of them alone, whose offsets are small, gives the same bits."""
+    L, H, G, P, N = 66000, 512, 8, 64, 128
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    d = {n: torch.randn(1, L, x, m, generator=gen, device="cuda", dtype=torch.bfloat16) * s
+         for n, x, m, s in (("q", G, N, 0.09), ("k", G, N, 0.09), ("v", H, P, 1.0))}
+    d["g"] = -0.3 * torch.rand(1, L, H, generator=gen, device="cuda")
+    d["beta"] = torch.rand(1, L, H, generator=gen, device="cuda")
+    dy = torch.randn(1, L, H, P, generator=gen, device="cuda", dtype=torch.bfloat16)
+    assert d["v"].numel() > 2 ** 31
+    last = {n: t[:, :, -(t.shape[2] // G):].contiguous() for n, t in d.items()}
+    y, f = ssd.delta_fwd(**d)
+    ys, fs = ssd.delta_fwd(**last)
+    hs = H // G
+    assert torch.isfinite(ys).all() and torch.equal(y[:, :, -hs:], ys) and torch.equal(f[:, -hs:], fs)
+    del y, ys
+    got = ssd.delta_bwd(**d, dy=dy)
+    want = ssd.delta_bwd(**last, dy=dy[:, :, -hs:].contiguous())
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert torch.equal(got[n][:, :, -want[n].shape[2]:], want[n]), n
+    torch.cuda.empty_cache()
+
+
+def test_step_offsets_past_32_bits():
+    b, H, P, N = 4096, 80, 64, 128
+    d, o, _, _ = make(1, 1, H, 1, P, N, "bf16", True, seed=18)
+    s = {n: t[:, 0].contiguous() for n, t in d.items()}
+    state = torch.zeros(b, H, P, N, device="cuda")
+    assert state.numel() > 2 ** 31
+    state[-1] = o["initial_states"][0]
+    many = {n: t.expand(b, *t.shape[1:]).contiguous() for n, t in s.items()}
+    y = ssd.delta_step(**many, state=state)
+    one = o["initial_states"].clone()
+    assert torch.equal(ssd.delta_step(**s, state=one)[0], y[-1]) and torch.equal(state[-1], one[0])
+    del state
+    torch.cuda.empty_cache()
+
+
+def test_many_ids():
+    """More ids than are ranked (2048) and more tokens than the run list keeps
+    flags of (65536), rows of different packing; most ids do not occur."""
+    lens = [[1 + (5 * i) % 31 for i in range(2600)], []]
+    L = sum(lens[0])
+    lens[1] = [7, L - 7]
+    ids = [3 * i for i in range(2602)]
+    assert 2 * L > 65536
+    d, o, dy, dfin = make(2, L, 2, 1, 16, 16, "bf16", True, seed=19, lens=lens, ids=ids)
+    o["num_seqs"] += 100
+    dfin = torch.cat([dfin, dfin[:100]])
+    _, f = check_fwd(d, o)
+    assert not f[1].any() and not f[-1].any()
+    check_bwd(d, o, dy, dfin)
+
+
+def test_initial_gradient_without_initial_states():
+    d, o, dy, dfin = make(2, 90, 4, 2, 16, 32, "f32", True, seed=20)
+    z = dict(o, initial_states=torch.zeros_like(o["initial_states"]))
+    got = ssd.delta_bwd(**d, dy=dy, dfinal_states=dfin, want_dinitial_states=True)
+    want = ssd.delta_bwd(**d, dy=dy, **z, dfinal_states=dfin)
+    assert torch.equal(got["dinitial_states"], want["dinitial_states"])
+    assert all(rel(got[n], want[n]) <= F32 for n in got)
+
+
+def test_two_host_threads():
+    from concurrent.futures import ThreadPoolExecutor
+    sets = [make(1, 200 + 50 * i, 4, 2, 64, 64, "bf16", True, seed=21 + i) for i in range(2)]
+    want = [ssd.delta_fwd(**d, **o) for d, o, _, _ in sets]
+    torch.cuda.synchronize()
+
+    def run(i):
+        d, o, _, _ = sets[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            r = [ssd.delta_fwd(**d, **o) for _ in range(20)]
+            torch.cuda.current_stream().synchronize()
+        return all(torch.equal(x, w) for p in r for x, w in zip(p, want[i]))
+
+    with ThreadPoolExecutor(2) as pool:
+        assert all(pool.map(run, range(2)))
+
+
+def test_training_step_captured():
+    """Forward and backward of both operators in one graph, replayed on new inputs."""
+    def step(v, w, rest):
+        y, _ = ssd.delta_chunked(rest["q"], rest["k"], v, rest["g"], rest["beta"])
+        return torch.autograd.grad((ssd.gated_layer_norm(y, w).float() ** 3).sum(), (v, w))
+
+    d, _, _, _ = make(1, 100, 4, 2, 64, 64, "bf16", seed=23)
+    e, _, _, _ = make(1, 100, 4, 2, 64, 64, "bf16", seed=24)
+    v, w = d["v"].requires_grad_(), torch.rand(64, device="cuda").requires_grad_()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(v, w, d)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(v, w, d)
+    with torch.no_grad():
+        for n in d:
+            d[n].copy_(e[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, step(v, w, d)))

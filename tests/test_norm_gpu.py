@@ -159,3 +159,25 @@ def test_gradients_against_differences():
 
         q = (loss(1e-4) - loss(-1e-4)) / 2e-4
         assert abs((leaf.grad.double() * u).sum().item() - q) <= 1e-5 * leaf.grad.norm().item() + 1e-6
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [7, 64, 130, 300, 1000, 1024, 2048, 5120, 8192, 16384, 20001])
+def test_in_place(cols, dtype):
+    """out may be x or z itself, whichever kernel the width takes."""
+    x, w, b, z, _ = make(700, cols, dtype, True, True, seed=9)
+    y = ssd.layer_norm(x, w, b, z=z)
+    for at in (x.clone(), z.clone()):
+        args = (at, z) if torch.equal(at, x) else (x, at)
+        assert torch.equal(ssd.layer_norm(args[0], w, b, z=args[1], out=at), y)
+
+
+@pytest.mark.parametrize("rows,cols", [(450000, 5120), (36000000, 64)])
+def test_offsets_past_32_bits(rows, cols):
+    x = torch.randn(rows, cols, device="cuda", dtype=torch.bfloat16)
+    assert x.numel() > 2 ** 31
+    w = torch.rand(cols, device="cuda")
+    end = x[-100:].clone()
+    assert torch.equal(ssd.layer_norm(x, w)[-100:], ssd.layer_norm(end, w))
+    assert torch.equal(ssd.layer_norm_bwd(x, w, None, x)[0][-100:], ssd.layer_norm_bwd(end, w, None, end)[0])
+    torch.cuda.empty_cache()

@@ -502,12 +502,16 @@ SSD_API ssd_status ssd_bwd(const ssd_bwd_args* args, void* stream);
  * The result is computed in chunks of 32 tokens, whose triangular systems are
  * inverted once and applied on the tensor cores; the operands carry 22 bits
  * (11 for what only y's rounding to bf16 sees), the sums 32.  It equals the
- * recurrence up to rounding.  Every input must be finite, but for g, where -inf is
- * a decay of zero: a value that is not finite can make the outputs of its
- * head from up to 31 tokens before it undefined.  Sizes: any dstate up to
- * 256 and any headdim up to 65536, batch * seqlen below 2^31.  Tensors on
- * 16-byte boundaries whose rows are multiples of 16 bytes are read with wide
- * loads, others element by element. */
+ * recurrence up to rounding, which is relative to the largest magnitudes of a
+ * chunk: of q and of k, and for each row of headdim of v - exp(g) S k.  Every
+ * input must be finite, but for g, where -inf is a decay of zero: a value that
+ * is not finite can make the outputs of its head from up to 31 tokens before
+ * it undefined.  So padding should hold ordinary values (zeros, say) or, with
+ * seq_idx, have an id of its own: sequences do not share chunks.  Sizes: any
+ * dstate up to 256 and any headdim up to 65536, batch * seqlen below 2^31.
+ * q, k and the output are accessed 16 bytes at a time where they start on
+ * 16-byte boundaries and their rows are multiples of 16 bytes, else element by
+ * element; v and dy that are not so placed are copied to rows that are. */
 typedef struct {
   int64_t batch, seqlen, nheads, headdim, dstate, ngroups;
   ssd_dtype dtype;             /* of q, k, v and y                               */
@@ -537,8 +541,8 @@ typedef struct {
  * invalid. */
 SSD_API size_t ssd_delta_fwd_workspace_size(const ssd_delta_args* args);
 
-/* Enqueue the forward on `stream`: two kernels, and one before them with
- * seq_idx.  SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_WORKSPACE as
+/* Enqueue the forward on `stream`: two kernels, and before them one with
+ * seq_idx and one where v is copied.  SSD_ERR_INVALID_ARG, SSD_ERR_UNSUPPORTED, SSD_ERR_WORKSPACE as
  * for ssd_fwd, with nothing enqueued; SSD_ERR_CUDA when a launch fails.
  * Outputs must not overlap the inputs. */
 SSD_API ssd_status ssd_delta_fwd(const ssd_delta_args* args, void* stream);

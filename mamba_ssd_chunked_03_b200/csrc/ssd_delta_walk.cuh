@@ -19,6 +19,22 @@
 // place; every eighth chunk it starts anew from the true maximum, so that it
 // does not run away where nothing decays.  Taking the maximum in every chunk
 // was measured too: 130 clocks a chunk and warp of 2970.
+//
+// Bound by the chain of a warp's chunk, about 1250 instructions that mostly
+// wait for one another: alone on its scheduler (128 CTAs: b4 L2048 H32 P64
+// N128, without y: 149 us) a warp issues in 29 % of the clocks and holds the
+// matrix pipe for 28 %.  Three CTAs an SM fill the gaps of one another: b8
+// L2048 H80 P64 N128 takes 460 us, 1.45 us a CTA and chunk against 2.0 alone;
+// the matrix instructions by themselves (184 a warp and chunk, 8 clocks each)
+// would take 214 us there.  Warp-level instructions run at a quarter of the
+// rate of tcgen05 (557 TFLOP/s measured), but their results go from product
+// to product in registers; on tcgen05 each of the five dependent products
+// would pass through TMEM and shared memory.  That form was not built, so how
+// it compares is not known.  Measured and not kept: issuing the
+// next chunk's copies between the products of this one (471 us), an explicit
+// order of loads before their use, units brought up to date only when they
+// run out (both no change), V read element by element where it is unaligned
+// (4.1 us a chunk; see k_delta_pad).
 #pragma once
 
 #include "ssd_delta_prep.cuh"

@@ -13,7 +13,9 @@
 // way.  The backward's partial sums (one set a CTA) are added by a second
 // kernel in a fixed order.  Rows wider than the registers hold are swept
 // several times from memory instead, with the column sums in a pass of their
-// own.
+// own.  1.3 M rows of 64, gated, bf16: 87 us, 5.8 TB/s; 100003 rows of
+// 129, gated, fp32, backward: 65 us, 4.0 TB/s (bound by the instructions of its
+// four-byte loads); 7 rows of 5120: 3.7 us, a chain of latencies.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -372,7 +374,8 @@ __device__ __forceinline__ void copy16(void* to, const void* from) {
 // registers to the column sums, and room for two rows at a time where a row has
 // two tensors at most: what takes the time is the chain of a row's sums through
 // the barrier, and two rows share one.  (16384 rows of 5120, backward: 138 us
-// with rows held in registers, 122 us from the ring one at a time.)
+// with rows held in registers, 122 us from the ring one at a time, 117 us two
+// at a time: 4.3 TB/s.  Three CTAs an SM with half the ring took 133 us.)
 template <int VPL, bool BWD, bool GATE>
 struct RowRing {
   static constexpr int kTensors = 1 + GATE + BWD;

@@ -810,31 +810,39 @@ def _call(entry, args, device: torch.device) -> None:
         raise SSDError(st)
 
 
-def _check_tensors(dev: torch.device, **named) -> None:
-    if dev.type != "cuda":
+def _check_tensors(first: torch.Tensor, *others, names: tuple) -> None:
+    """``first`` and the ``others`` (None: not given) contiguous on one device."""
+    index = first.get_device()
+    if index < 0:
         raise ValueError("the tensors must be CUDA tensors")
-    for name, t in named.items():
-        if t is not None and (t.device != dev or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+    for i, t in enumerate((first, *others)):
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            raise ValueError(f"{names[i]} must be a contiguous CUDA tensor on {first.device}")
+
+
+def _check_dtypes(q, k, v) -> None:
+    t = v.dtype
+    if (t is not torch.bfloat16 and t is not torch.float32) or q.dtype is not t or k.dtype is not t:
+        raise TypeError("q, k and v must all be float32 or all bfloat16")
 
 
 def _check_delta(q, k, v, g, beta, initial_states, seq_idx):
     if q.dim() != 4 or v.dim() != 4 or k.shape != q.shape:
         raise ValueError("expected q and k (b,L,G,N), v (b,L,H,P), g and beta (b,L,H)")
     b, L, H, P = v.shape
-    G, N = q.shape[2], q.shape[3]
-    if q.shape[0] != b or q.shape[1] != L or tuple(g.shape) != (b, L, H) or tuple(beta.shape) != (b, L, H):
+    qb, qL, G, N = q.shape
+    if qb != b or qL != L or g.shape != (b, L, H) or beta.shape != (b, L, H):
         raise ValueError("shapes do not match q and k (b,L,G,N), v (b,L,H,P), g and beta (b,L,H)")
-    if v.dtype not in (torch.float32, torch.bfloat16) or q.dtype != v.dtype or k.dtype != v.dtype:
-        raise TypeError("q, k and v must all be float32 or all bfloat16")
-    if g.dtype != torch.float32 or beta.dtype != torch.float32:
+    _check_dtypes(q, k, v)
+    if g.dtype is not torch.float32 or beta.dtype is not torch.float32:
         raise TypeError("g and beta must be float32")
     if initial_states is not None and (initial_states.dtype != torch.float32
                                        or tuple(initial_states.shape) != (b, H, P, N)):
         raise ValueError("initial_states must be float32 (b, H, P, N)")
     if seq_idx is not None and (seq_idx.dtype != torch.int32 or tuple(seq_idx.shape) != (b, L)):
         raise ValueError("seq_idx must be int32 (b, L)")
-    _check_tensors(v.device, q=q, k=k, v=v, g=g, beta=beta, initial_states=initial_states, seq_idx=seq_idx)
+    _check_tensors(v, q, k, g, beta, initial_states, seq_idx,
+                   names=("v", "q", "k", "g", "beta", "initial_states", "seq_idx"))
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -930,7 +938,7 @@ def delta_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
     if dfinal_states is not None and (dfinal_states.dtype != torch.float32
                                       or tuple(dfinal_states.shape) != (rows, H, P, N)):
         raise ValueError(f"dfinal_states must be float32 {(rows, H, P, N)}")
-    _check_tensors(v.device, dy=dy, dfinal_states=dfinal_states)
+    _check_tensors(v, dy, dfinal_states, names=("v", "dy", "dfinal_states"))
     if want_dinitial_states is None:
         want_dinitial_states = initial_states is not None
     d = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v), "dg": torch.empty_like(g),
@@ -989,14 +997,13 @@ def delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     if q.dim() != 3 or v.dim() != 3 or k.shape != q.shape:
         raise ValueError("expected q and k (b,G,N), v (b,H,P), g and beta (b,H), state (b,H,P,N)")
     b, H, P = v.shape
-    G, N = q.shape[1], q.shape[2]
-    if q.shape[0] != b or tuple(g.shape) != (b, H) or tuple(beta.shape) != (b, H) or tuple(state.shape) != (b, H, P, N):
+    qb, G, N = q.shape
+    if qb != b or g.shape != (b, H) or beta.shape != (b, H) or state.shape != (b, H, P, N):
         raise ValueError("shapes do not match q and k (b,G,N), v (b,H,P), g and beta (b,H), state (b,H,P,N)")
-    if v.dtype not in (torch.float32, torch.bfloat16) or q.dtype != v.dtype or k.dtype != v.dtype:
-        raise TypeError("q, k and v must all be float32 or all bfloat16")
-    if g.dtype != torch.float32 or beta.dtype != torch.float32 or state.dtype != torch.float32:
+    _check_dtypes(q, k, v)
+    if g.dtype is not torch.float32 or beta.dtype is not torch.float32 or state.dtype is not torch.float32:
         raise TypeError("g, beta and state must be float32")
-    _check_tensors(v.device, q=q, k=k, v=v, g=g, beta=beta, state=state)
+    _check_tensors(v, q, k, g, beta, state, names=("v", "q", "k", "g", "beta", "state"))
     y = _output_like(y, "y", v)
     a = DeltaStepArgs(b, H, P, N, G, _dtype(v), N ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(),
                       v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), y.data_ptr())
@@ -1016,7 +1023,7 @@ def _check_norm(x, weight, bias, z) -> None:
         raise ValueError(f"bias must be float32 ({cols},)")
     if z is not None and (z.dtype != x.dtype or z.shape != x.shape):
         raise ValueError("z must be like x")
-    _check_tensors(x.device, x=x, weight=weight, bias=bias, z=z)
+    _check_tensors(x, weight, bias, z, names=("x", "weight", "bias", "z"))
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -1043,7 +1050,7 @@ def layer_norm_bwd(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Option
     _check_norm(x, weight, bias, z)
     if dout.dtype != x.dtype or dout.shape != x.shape:
         raise ValueError("dout must be like x")
-    _check_tensors(x.device, dout=dout)
+    _check_tensors(x, dout, names=("x", "dout"))
     cols = x.shape[-1]
     want_dweight = weight is not None if want_dweight is None else want_dweight
     want_dbias = bias is not None if want_dbias is None else want_dbias

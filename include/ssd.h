@@ -506,8 +506,9 @@ SSD_API ssd_status ssd_bwd(const ssd_bwd_args* args, void* stream);
  * chunk: of q and of k, and for each row of headdim of v - exp(g) S k.  Every
  * input must be finite, but for g, where -inf is a decay of zero: a value that
  * is not finite can make the outputs of its head from up to 31 tokens before
- * it undefined.  So padding should hold ordinary values (zeros, say) or, with
- * seq_idx, have an id of its own: sequences do not share chunks.  Sizes: any
+ * it undefined.  So padding should hold ordinary values (zeros, say; with g and
+ * beta zero it leaves the state as it was) or, with seq_idx, have an id of its
+ * own: sequences do not share chunks.  Sizes: any
  * dstate up to 256 and any headdim up to 65536, batch * seqlen below 2^31.
  * q, k and the output are accessed 16 bytes at a time where they start on
  * 16-byte boundaries and their rows are multiples of 16 bytes, else element by

@@ -31,7 +31,10 @@
 // to product in registers; on tcgen05 each of the five dependent products
 // would pass through TMEM and shared memory.  That form was not built, so how
 // it compares is not known.  Measured and not kept: issuing the
-// next chunk's copies between the products of this one (471 us), an explicit
+// next chunk's copies between the products of this one (471 us), two warps for
+// 16 rows, half of the columns each, for calls of few CTAs (their exchange and
+// the products that both make cost more than the halves save: 16 chunks of
+// fp32 take 45 us against 34, the reverse walk 263 against 220), an explicit
 // order of loads before their use, units brought up to date only when they
 // run out (both no change), V read element by element where it is unaligned
 // (4.1 us a chunk; see k_delta_pad).

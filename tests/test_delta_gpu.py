@@ -495,3 +495,27 @@ def test_training_step_captured():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(got, step(v, w, d)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_padded_batch(dtype):
+    """Rows of 100, 33 and 1 tokens padded to 130: padding with g and beta zero
+    neither reaches back nor moves the state, whatever q, k and v hold there."""
+    d, o, dy, dfin = make(3, 130, 4, 2, 24, 32, dtype, True, seed=25)
+    lens = [100, 33, 1]
+    for i, n in enumerate(lens):
+        d["g"][i, n:] = 0
+        d["beta"][i, n:] = 0
+        dy[i, n:] = 0
+    y, f = ssd.delta_fwd(**d, initial_states=o["initial_states"])
+    got = ssd.delta_bwd(**d, dy=dy, initial_states=o["initial_states"], dfinal_states=dfin)
+    for i, n in enumerate(lens):
+        one = {m: t[i:i + 1, :n].contiguous() for m, t in d.items()}
+        h0 = o["initial_states"][i:i + 1].contiguous()
+        ys, fs = ssd.delta_fwd(**one, initial_states=h0)
+        # both are within the tolerance of the same recurrence
+        assert rel(y[i:i + 1, :n], ys) <= 2 * tol(ys) and rel(f[i:i + 1], fs) <= 2 * F32
+        want = ssd.delta_bwd(**one, dy=dy[i:i + 1, :n].contiguous(), initial_states=h0, dfinal_states=dfin[i:i + 1].contiguous())
+        for m in ("dq", "dk", "dv", "dg", "dbeta"):
+            assert rel(got[m][i:i + 1, :n], want[m]) <= 2 * tol(want[m]), m
+        assert rel(got["dinitial_states"][i:i + 1], want["dinitial_states"]) <= 2 * F32

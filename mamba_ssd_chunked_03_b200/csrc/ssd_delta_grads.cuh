@@ -31,6 +31,7 @@
 // against 461 at that step, since P and Z are then formed twice.
 #pragma once
 
+#include "ssd_delta_blocks.h"
 #include "ssd_delta_prep.cuh"
 
 namespace ssd {
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
   // chunk, and beta, as they were copied; exp(cs) and exp(cs_C - cs) over all 64
   __shared__ __align__(16) float intol[kCheck], outl[kCheck], inv[kCheck], bet[kCheck], into[kCheck], outof[kCheck];
   __shared__ __align__(16) float most[5][8];  // largest magnitudes: chunk (2), 16 columns of headdim (4)
-  __shared__ float whole[2];
+  __shared__ float whole[2];  // of the chunks that exist
   __shared__ int plain[2];
   __shared__ float scale[5], iscale[5];       // of Y, E, D, S, dS
   __shared__ float sums[6][kCheck];           // d.e, dv.v, and q.dq of each quarter of the columns
@@ -475,7 +476,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
     // token that is summed over.  A block's rows are in one chunk, its columns too.
     const float kt = mt < 2 ? ik0 : ik1, ks = sb < 2 ? ik0 : ik1, qt = mt < 2 ? iq0 : iq1;
     float m1 = 0.f, m3 = 0.f;
-    if (sb <= mt) {
+    // Blocks of a second chunk that does not exist stay zero, as their rows of
+    // the operands are: it has no decays to read.
+    if (block_exists(mt, sb, nch)) {
       const bool cross = (mt >> 1) != (sb >> 1), simple = cross || plain[mt >> 1];
       const float* cf = cross ? outl : inv;
 #pragma unroll

@@ -501,7 +501,7 @@ SSD_API ssd_status ssd_bwd(const ssd_bwd_args* args, void* stream);
  *
  * The result is computed in chunks of 32 tokens, whose triangular systems are
  * inverted once and applied on the tensor cores; the operands carry 22 bits
- * (11 for what only y's rounding to bf16 sees), the sums 32.  It equals the
+ * and the sums 32 in either type, and y is rounded once.  It equals the
  * recurrence up to rounding, which is relative to the largest magnitudes of a
  * chunk: of q and of k, and for each row of headdim of v - exp(g) S k.  Every
  * input must be finite, but for g, where -inf is a decay of zero: a value that

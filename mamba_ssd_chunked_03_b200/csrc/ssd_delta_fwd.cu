@@ -9,7 +9,7 @@ using namespace ssd::delta;
 namespace {
 
 size_t head_tiles_bytes(const Shape& s) {
-  return (size_t)s.chunks * s.H * (s.bf16 ? HeadTiles<1>::kStride : HeadTiles<2>::kStride);
+  return (size_t)s.chunks * s.H * HeadTiles<2>::kStride;
 }
 
 }  // namespace

@@ -24,8 +24,8 @@
 // A, its inverse by substitution with a row in each lane (496 steps of one
 // FMA, the column of A broadcast from shared memory), M.  Bound by issue and
 // the latency of shared memory in the substitution (issue slots 41 % busy, six
-// CTAs an SM): b8 L2048 H80 N128, 40960 heads of chunks (284 MB
-// written), 139 us, 2.0 TB/s.
+// CTAs an SM): b8 L2048 H80 N128, 40960 heads of chunks (368 MB
+// written), 158 us, 2.3 TB/s.
 #pragma once
 
 #include "ssd_delta.cuh"
@@ -77,7 +77,7 @@ struct HeadTiles {
   static constexpr int kStride = kBytes + (DECAYS ? (int)sizeof(Decays) : 0);
 };
 using RevTiles = HeadTiles<2, true>;
-static_assert(HeadTiles<1>::kBytes % 16 == 0, "16-byte copies");
+static_assert(HeadTiles<2>::kBytes % 16 == 0, "16-byte copies");
 
 struct PrepArgs {
   int64_t L, H, G, N, hpg;
@@ -129,18 +129,17 @@ __device__ __forceinline__ float store_row(const float (&t)[kC], int lane, char*
     for (int e = 0; e < 4; ++e) split2(mul2(t[c + 2 * e], t[c + 2 * e + 1], sc), hi[e], lo[e]);
     const uint32_t o = tile_off<32>(lane, c);
     *reinterpret_cast<uint4*>(hi_tile + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    if (lo_tile) *reinterpret_cast<uint4*>(lo_tile + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(lo_tile + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
   return inv;
 }
 
-// FWD, REV: which walk's tiles are made; MT: terms of M.
+// FWD, REV: which walk's tiles are made.
 template <typename T, int NT, bool FWD, bool REV>
 __global__ void __launch_bounds__(kPrepThreads, NT * sizeof(T) <= 256 ? 6 : 3) k_delta_prep(const PrepArgs a) {
   using X = TokenTiles<T, NT>;
-  constexpr int MT = REV || sizeof(T) == 4 ? 2 : 1;
   constexpr bool kFwdM = !REV;  // the backward's forward walk makes no y
-  using HF = HeadTiles<kFwdM ? MT : 0>;
+  using HF = HeadTiles<kFwdM ? 2 : 0>;
   using HR = RevTiles;
   constexpr int E = 16 / (int)sizeof(T), PC = NT / E, V = kC * NT / E / kPrepThreads;
   extern __shared__ __align__(128) char sm[];
@@ -354,7 +353,7 @@ __global__ void __launch_bounds__(kPrepThreads, NT * sizeof(T) <= 256 ? 6 : 3) k
       if (rev || kFwdM) {
         row(gq, a.scale, 0, [&](int cidx, float w) { t[cidx] = w; });
         char* mi = img + (rev ? HR::kM : HF::kM);
-        f->mu[lane] = store_row(t, lane, mi, (rev ? 2 : MT) == 2 ? mi + kSq : nullptr);
+        f->mu[lane] = store_row(t, lane, mi, mi + kSq);
         f->qc[lane] = qc;
         if (rev) {
           Decays* d = reinterpret_cast<Decays*>(img + HR::kBytes);

@@ -24,12 +24,14 @@
 // wait for one another: alone on its scheduler (128 CTAs: b4 L2048 H32 P64
 // N128, without y: 149 us) a warp issues in 29 % of the clocks and holds the
 // matrix pipe for 28 %.  Three CTAs an SM fill the gaps of one another: b8
-// L2048 H80 P64 N128 takes 460 us, 1.45 us a CTA and chunk against 2.0 alone;
-// the matrix instructions by themselves (184 a warp and chunk, 8 clocks each)
-// would take 214 us there.  Warp-level instructions run at a quarter of the
-// rate of tcgen05 (557 TFLOP/s measured), but their results go from product
-// to product in registers; on tcgen05 each of the five dependent products
-// would pass through TMEM and shared memory.  That form was not built, so how
+// L2048 H80 P64 N128 takes 525 us; the matrix instructions by themselves (228 a
+// warp and chunk, 8 clocks each) would take 265 us there.  A third of them are
+// y's.  With one term of S, U and M for y in bf16 (184 instructions, errors of
+// 2^-12 before y's own rounding) the walk took 460 us; it is not kept, so that y
+// is the rounding of a value held to 32 bits.  Warp-level instructions run at a
+// quarter of the rate of tcgen05 (557 TFLOP/s measured), but their results go
+// from product to product in registers; on tcgen05 each of the five dependent
+// products would pass through TMEM and shared memory.  That form was not built, so how
 // it compares is not known.  Measured and not kept: issuing the
 // next chunk's copies between the products of this one (471 us), two warps for
 // 16 rows, half of the columns each, for calls of few CTAs (their exchange and
@@ -449,7 +451,7 @@ __device__ __forceinline__ void state_times(const float (&S)[NT / 8][4], float (
     for (int x = 0; x < 4; ++x)
       split2(make_float2(S[2 * ks + (x >> 1)][2 * (x & 1)], S[2 * ks + (x >> 1)][2 * (x & 1) + 1]), hi[x], lo[x]);
     tokens_mma<NT, TERMS, true>(acc, hi, lo, kt, ks, lane);
-    if constexpr (Y) tokens_mma<NT, TERMS, TERMS == 2>(y, hi, lo, qt, ks, lane);
+    if constexpr (Y) tokens_mma<NT, TERMS, true>(y, hi, lo, qt, ks, lane);
   }
 }
 
@@ -499,7 +501,7 @@ __device__ __forceinline__ void lower_mma_t(float (&d)[4][4], const uint32_t (&h
 template <typename T, int NT, int MODE>
 __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(const WalkArgs a) {
   constexpr bool kY = MODE == kForward;
-  constexpr int kMTerms = !kY ? 0 : sizeof(T) == 4 ? 2 : 1;
+  constexpr int kMTerms = kY ? 2 : 0;  // M to 22 bits, as every operand that is a result
   using B = Buffers<T, NT, kY, kMTerms>;
   using X = TokenTiles<T, NT>;
   using Hd = HeadTiles<kMTerms>;
@@ -568,10 +570,10 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(cons
     const int n = run.len - j * kC < kC ? run.len - j * kC : kC;
     const int64_t th = (run.tok + (int64_t)j * kC) * a.H + h, row0 = th * a.P + p0, rowe = th * a.pe + p0;
     if constexpr (kY) {
-      as_operand<kTerms == 2>(e, hi, lo);
+      as_operand<true>(e, hi, lo);
       scale_tile(y, f.qc, unit.sig, lane);
       zero(acc);
-      lower_mma<kTerms == 2, kMTerms>(acc, hi, lo, mt, lane);
+      lower_mma<true, kMTerms>(acc, hi, lo, mt, lane);
       add_scaled(y, acc, f.mu, iv, lane);
       store_tile<T>(y, stage, static_cast<T*>(a.out) + row0, a.H * a.P, n, rows, a.out_vec, lane);
     } else {
@@ -595,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_walk(cons
 
 template <typename T, int NT, int MODE>
 cudaError_t launch_walk_nt(const WalkArgs& a, cudaStream_t stream) {
-  constexpr int smem = Buffers<T, NT, MODE == kForward, MODE != kForward ? 0 : sizeof(T) == 4 ? 2 : 1>::kBytes;
+  constexpr int smem = Buffers<T, NT, MODE == kForward, MODE == kForward ? 2 : 0>::kBytes;
   static_assert(smem <= 227 * 1024, "shared memory");
   static std::atomic<uint64_t> seen{0};
   return launch_kernel(k_delta_walk<T, NT, MODE>, seen, (unsigned)a.units, kThreads, smem, smem, true, stream, a);

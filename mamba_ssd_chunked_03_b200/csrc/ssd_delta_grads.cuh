@@ -13,8 +13,10 @@
 // (pi_{t-1} = dg_t + dy_{t-1}.y_{t-1}, dg_t = pi_t - dv_t.v_t, and dy.y = dq.q).
 // <dS, S> is known at both ends of the 64 tokens (dg_0 is that of the tokens
 // before), so the sums run from the nearer end, over 32 tokens at most, and
-// rounding does not pile up along the sequence.  dq is therefore held to fp32
-// accuracy (split operands), dk only to its type's.
+// rounding does not pile up along the sequence.  All operands that are results
+// are split in two terms: dg needs dq to fp32 accuracy, and what is returned is
+// rounded once.  (One term for dk's in bf16, errors of 2^-12 before its own
+// rounding: 354 us where it now takes 414.)
 //
 // One CTA takes 64 tokens of a group, a slice of the columns n, and some of the
 // group's heads, whose dq and dk it adds in registers in a fixed order; sixteen
@@ -22,7 +24,7 @@
 // twice the columns each took 1.24 times as long: between its barriers a warp's
 // instructions depend on one another, and two warps a scheduler do not fill it.)
 //
-// b4 L2048 H32 G8 P64 N128: 354 us, 543 MB from HBM (1.5 TB/s).  Bound by
+// b4 L2048 H32 G8 P64 N128: 414 us, 543 MB from HBM (1.3 TB/s).  Bound by
 // latency between its barriers: the tiles of a head take 220 KB, so one CTA an
 // SM, whose sixteen warps issue in 42 % of the clocks and keep the matrix pipe
 // busy for 18 %; what waits is fixed latencies (1.7 clocks an instruction),
@@ -76,24 +78,27 @@ struct GradArgs {
 // Sizes of the shared tiles of k_delta_grads, in bytes.
 template <typename T, int NT>
 struct GradTiles {
-  static constexpr int kTerms = sizeof(T) == 2 ? 1 : 2;
+  static constexpr int kTerms = sizeof(T) == 2 ? 1 : 2;  // of k, q and dY; what is a result has two
   static constexpr int kNS = sizeof(T) == 4 || NT == 64 ? 64 : 128;  // columns n of a CTA
   static constexpr int kTok = 64 * kNS * 2, kSmall = 64 * 64 * 2;
   static constexpr int kK = 0, kQ = kK + kTerms * kTok;
   static constexpr int kS = kQ + kTerms * kTok;        // hi, lo
-  static constexpr int kDS = kS + 2 * kTok;            // terms
-  static constexpr int kE = kDS + kTerms * kTok;       // hi, lo
-  static constexpr int kD = kE + 2 * kSmall;           // terms
-  static constexpr int kY = kD + kTerms * kSmall;      // terms
-  static constexpr int kW1 = kY + kTerms * kSmall;     // P with k's scales, hi, lo
-  static constexpr int kW2 = kW1 + 2 * kSmall;         // P with q's scales, terms
-  static constexpr int kZa = kW2 + kTerms * kSmall;    // Z with k's scales by row
-  static constexpr int kZb = kZa + kTerms * kSmall;    // Z with k's scales by column
+  static constexpr int kDS = kS + 2 * kTok;            // hi, lo, as all that follow but Y
+  static constexpr int kE = kDS + 2 * kTok;
+  static constexpr int kD = kE + 2 * kSmall;
+  static constexpr int kY = kD + 2 * kSmall;           // terms
+  // P and Z of a head, once its pieces' E, D and dY are used up: in their place
+  static constexpr int kW1 = kE;                       // P with k's scales
+  static constexpr int kW2 = kW1 + 2 * kSmall;         // P with q's scales
+  static constexpr int kZa = kW2 + 2 * kSmall;         // Z with k's scales by row
+  static constexpr int kZb = kZa + 2 * kSmall;         // Z with k's scales by column
+  static constexpr int kEnd = kZb + 2 * kSmall;
+  static_assert(kY + kTerms * kSmall <= kEnd, "the operands of a piece");
   // E, D, V and dY of the next piece as they are in memory
-  static constexpr int kRawE = kZb + kTerms * kSmall, kRawD = kRawE + 64 * 64 * 4;
+  static constexpr int kRawE = kEnd, kRawD = kRawE + 64 * 64 * 4;
   static constexpr int kRawV = kRawD + 64 * 64 * 4, kRawY = kRawV + 64 * 64 * (int)sizeof(T);
   static constexpr int kRawEnd = kRawY + 64 * 64 * (int)sizeof(T);
-  // two terms of everything leave no room for them: they are read when needed
+  // fp32 pieces are read when they are needed
   static constexpr bool kAhead = sizeof(T) == 2;
   static constexpr int kBytes = kAhead ? kRawEnd : kRawE;
 };
@@ -383,7 +388,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
           state_at(i, p0, p, n);
           const uint32_t to = tile_off<NS>(p, n);
           put4<2>(sm + G::kS, G::kTok, to, xs[i], scale[3]);
-          put4<TM>(sm + G::kDS, G::kTok, to, xd[i], scale[4]);
+          put4<2>(sm + G::kDS, G::kTok, to, xd[i], scale[4]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) pi = fmaf(xd[i][e], xc[i][e], pi);
         }
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
         if ((lane & 15) == 0) sums[0][t] += de, sums[1][t] += dv;  // one thread of its own for each t
         const uint32_t to = tile_off<64>(t, p);
         put4<2>(sm + G::kE, G::kSmall, to, e4, scale[1]);
-        put4<TM>(sm + G::kD, G::kSmall, to, d4, scale[2]);
+        put4<2>(sm + G::kD, G::kSmall, to, d4, scale[2]);
         put4<TM>(sm + G::kY, G::kSmall, to, y4, scale[0]);
       }
       __syncthreads();
@@ -430,12 +435,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
         const int br = (lane & 7) + (lane >> 4) * 8, bc = ((lane >> 3) & 1) * 8;
 #pragma unroll
         for (int k = 0; k < kPS / 16; ++k) {
-          uint32_t Y[TM][4], D[TM][4], E[2][4];
+          uint32_t Y[TM][4], D[2][4], E[2][4];
 #pragma unroll
-          for (int t = 0; t < TM; ++t) {
-            a_frag<64, false>(smu + G::kY + t * G::kSmall, 16 * mt, 16 * k, lane, Y[t]);
-            a_frag<64, false>(smu + G::kD + t * G::kSmall, 16 * mt, 16 * k, lane, D[t]);
-          }
+          for (int t = 0; t < TM; ++t) a_frag<64, false>(smu + G::kY + t * G::kSmall, 16 * mt, 16 * k, lane, Y[t]);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) a_frag<64, false>(smu + G::kD + t * G::kSmall, 16 * mt, 16 * k, lane, D[t]);
 #pragma unroll
           for (int t = 0; t < 2; ++t) ldsm4(smu + G::kE + t * G::kSmall + tile_off<64>(16 * sb + br, 16 * k + bc), E[t]);
 #pragma unroll
@@ -443,11 +447,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
             mma(x[i], Y[0], E[0][2 * i], E[0][2 * i + 1]);
             mma(z[i], D[0], E[0][2 * i], E[0][2 * i + 1]);
             mma(x[i], Y[0], E[1][2 * i], E[1][2 * i + 1]);
-            if constexpr (TM == 2) {
-              mma(x[i], Y[TM - 1], E[0][2 * i], E[0][2 * i + 1]);
-              mma(z[i], D[0], E[1][2 * i], E[1][2 * i + 1]);
-              mma(z[i], D[TM - 1], E[0][2 * i], E[0][2 * i + 1]);
-            }
+            mma(z[i], D[0], E[1][2 * i], E[1][2 * i + 1]);
+            if constexpr (TM == 2) mma(x[i], Y[TM - 1], E[0][2 * i], E[0][2 * i + 1]);
+            mma(z[i], D[1], E[0][2 * i], E[0][2 * i + 1]);
           }
         }
         add_rows(P, x, iy * ie, iy * ie);
@@ -460,10 +462,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
       product<TN, 64, false, TM, NS, 2>(tmp, smu + G::kY, G::kSmall, 16 * mt, smu + G::kS, G::kTok, nb, 0, kPS / 16, lane);
       add_rows(dqh, tmp, a.scale * in0 * (iy * is), a.scale * in1 * (iy * is));
       clear(tmp);
-      product<TN, 64, false, TM, NS, TM>(tmp, smu + G::kD, G::kSmall, 16 * mt, smu + G::kS, G::kTok, nb, 0, kPS / 16, lane);
+      product<TN, 64, false, 2, NS, 2>(tmp, smu + G::kD, G::kSmall, 16 * mt, smu + G::kS, G::kTok, nb, 0, kPS / 16, lane);
       add_rows(dk, tmp, -be0 * in0 * (id * is), -be1 * in1 * (id * is));
       clear(tmp);
-      product<TN, 64, false, TM, NS, TM>(tmp, smu + G::kE, G::kSmall, 16 * mt, smu + G::kDS, G::kTok, nb, 0, kPS / 16, lane);
+      product<TN, 64, false, 2, NS, 2>(tmp, smu + G::kE, G::kSmall, 16 * mt, smu + G::kDS, G::kTok, nb, 0, kPS / 16, lane);
       add_rows(dk, tmp, be0 * outof[r0] * (ie * ids), be1 * outof[r0 + 8] * (ie * ids));
       if (hn == h) {  // another piece of this head
         __syncthreads();
@@ -523,16 +525,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             const uint32_t o = tile_off<64>(r0 + 8 * hh, 16 * sb + 8 * i + 2 * (lane & 3));
-            const auto put = [&](int at, bool two, float2 x) {
+            const auto put = [&](int at, float2 x) {
               uint32_t hi, lo;
               split2(x, hi, lo);
               *reinterpret_cast<uint32_t*>(sm + at + o) = hi;
-              if (two) *reinterpret_cast<uint32_t*>(sm + at + G::kSmall + o) = lo;
+              *reinterpret_cast<uint32_t*>(sm + at + G::kSmall + o) = lo;
             };
-            put(G::kW1, true, mul2(P[i][2 * hh], P[i][2 * hh + 1], f1));
-            put(G::kW2, TM == 2, mul2(P[i][2 * hh], P[i][2 * hh + 1], f2));
-            put(G::kZa, TM == 2, mul2(Z[i][2 * hh], Z[i][2 * hh + 1], fa));
-            put(G::kZb, TM == 2, mul2(Z[i][2 * hh], Z[i][2 * hh + 1], fb));
+            put(G::kW1, mul2(P[i][2 * hh], P[i][2 * hh + 1], f1));
+            put(G::kW2, mul2(P[i][2 * hh], P[i][2 * hh + 1], f2));
+            put(G::kZa, mul2(Z[i][2 * hh], Z[i][2 * hh + 1], fa));
+            put(G::kZb, mul2(Z[i][2 * hh], Z[i][2 * hh + 1], fb));
           }
       }
     }
@@ -544,11 +546,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
       product<TN, 64, false, 2, NS, TM>(tmp, smu + G::kW1, G::kSmall, 16 * mt, smu + G::kK, G::kTok, nb, 0, mt + 1, lane);
       add_rows(dqh, tmp, i1, i1);
       clear(tmp);
-      product<TN, 64, true, TM, NS, TM>(tmp, smu + G::kW2, G::kSmall, 16 * mt, smu + G::kQ, G::kTok, nb, mt, 4, lane);
+      product<TN, 64, true, 2, NS, TM>(tmp, smu + G::kW2, G::kSmall, 16 * mt, smu + G::kQ, G::kTok, nb, mt, 4, lane);
       add_rows(dk, tmp, i2, i2);
       clear(tmp);
-      product<TN, 64, true, TM, NS, TM>(tmp, smu + G::kZa, G::kSmall, 16 * mt, smu + G::kK, G::kTok, nb, mt, 4, lane);
-      product<TN, 64, false, TM, NS, TM>(tmp, smu + G::kZb, G::kSmall, 16 * mt, smu + G::kK, G::kTok, nb, 0, mt + 1, lane);
+      product<TN, 64, true, 2, NS, TM>(tmp, smu + G::kZa, G::kSmall, 16 * mt, smu + G::kK, G::kTok, nb, mt, 4, lane);
+      product<TN, 64, false, 2, NS, TM>(tmp, smu + G::kZb, G::kSmall, 16 * mt, smu + G::kK, G::kTok, nb, 0, mt + 1, lane);
       add_rows(dk, tmp, i3, i3);
       // q.dq of this head
       float q0 = 0.f, q1 = 0.f;

@@ -52,3 +52,16 @@ def test_y_packed():
     a, kw = ref_args(d, o, 128 ** -0.5)
     got = beyond_half_a_step(y, delta(*a, **kw)[0])
     assert got <= F32, got
+
+
+@pytest.mark.parametrize("case", CASES, ids=ids)
+def test_gradients(case):
+    b, L, H, G, P, N, h0 = case
+    d, o, dy, dfin = make(b, L, H, G, P, N, "bf16", h0, seed=42)
+    got = ssd.delta_bwd(**d, dy=dy, **o, dfinal_states=dfin)
+    torch.cuda.synchronize()
+    a, kw = ref_args(d, o, N ** -0.5)
+    want = delta_grads(*a, dy, **kw, dfin=dfin)
+    for n in ("dq", "dk", "dv"):
+        off = beyond_half_a_step(got[n], want[n])
+        assert off <= F32, (n, off)

@@ -503,7 +503,8 @@ SSD_API ssd_status ssd_bwd(const ssd_bwd_args* args, void* stream);
  * inverted once and applied on the tensor cores; the operands carry 22 bits
  * and the sums 32 in either type, and y is rounded once.  It equals the
  * recurrence up to rounding, which is relative to the largest magnitudes of a
- * chunk: of q and of k, and for each row of headdim of v - exp(g) S k.  Every
+ * token's q and k, and for each row of headdim of its state (some 2^-29 of the
+ * row's largest value) and of a chunk's v - exp(g) S k.  Every
  * input must be finite, but for g, where -inf is a decay of zero: a value that
  * is not finite can make the outputs of its head from up to 31 tokens before
  * it undefined.  So padding should hold ordinary values (zeros, say; with g and

@@ -2,8 +2,8 @@
 // ssd_delta_bwd.cu): the run list, the warp-level matrix instruction, and the
 // operand split that keeps fp32 accuracy on 16-bit matrix instructions.
 //
-// Operands.  Every matrix operand is held as fp16 after its rows (for q and k:
-// the chunk's tile) have been brought into fp16's range by a power of two that
+// Operands.  Every matrix operand is held as fp16 after its rows (for the
+// gradients: its tile) have been brought into fp16's range by a power of two that
 // is folded back into the fp32 result.  A bf16 value is then exact in one term
 // (8 bits, down to 2^-17 of the largest, and off by 2^-25 of it below); an
 // fp32 one is split in two, hi + lo with 11 bits each, so that a product of an
@@ -70,7 +70,7 @@ __device__ __forceinline__ float pow2_scale(float m, float& inv) {
   return __uint_as_float((uint32_t)(268 - e) << 23);
 }
 
-// The same for tiles of q and k, brought to [1, 2): their products with a state
+// The same for rows of q and k, brought to [1, 2): their products with a state
 // of up to 2^14 then stay in its units (ssd_delta_walk.cuh).
 __device__ __forceinline__ float pow2_unit(float m, float& inv) {
   int e = (int)(__float_as_uint(m) >> 23);

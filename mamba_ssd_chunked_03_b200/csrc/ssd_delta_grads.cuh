@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
   // of the 64 tokens: exp(cs), exp(cs_C - cs), 1 / exp(cs) within their 32-token
   // chunk, and beta, as they were copied; exp(cs) and exp(cs_C - cs) over all 64
   __shared__ __align__(16) float intol[kCheck], outl[kCheck], inv[kCheck], bet[kCheck], into[kCheck], outof[kCheck];
+  __shared__ __align__(8) float ik[kCheck], iq[kCheck];  // 1 / scale of the tokens' k and q, the same for all heads
   __shared__ __align__(16) float most[5][8];  // largest magnitudes: chunk (2), 16 columns of headdim (4)
   __shared__ float whole[2];  // of the chunks that exist
   __shared__ int plain[2];
@@ -261,9 +262,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
       *reinterpret_cast<uint4*>(sm + dst) =
           r < kC * nch ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
     }
-  // 1 / scale of the chunks' k and q
-  const float ik0 = factors(0, h0)->ik, iq0 = factors(0, h0)->iq;
-  const float ik1 = nch == 2 ? factors(1, h0)->ik : ik0, iq1 = nch == 2 ? factors(1, h0)->iq : iq0;
+  if (threadIdx.x < kCheck) {
+    const int t = threadIdx.x;
+    ik[t] = t < kC * nch ? decays(t >> 5, h0)->ik[t & 31] : 1.f;
+    iq[t] = t < kC * nch ? decays(t >> 5, h0)->iq[t & 31] : 1.f;
+  }
   float dq[TN][4], dk[TN][4];
   clear(dq);
   clear(dk);
@@ -474,10 +477,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
         cp_async_commit();
       }
     }
-    // P and Z with their decays; the scale of the chunk's k or q goes with the
-    // token that is summed over.  A block's rows are in one chunk, its columns too.
-    const float kt = mt < 2 ? ik0 : ik1, ks = sb < 2 ? ik0 : ik1, qt = mt < 2 ? iq0 : iq1;
-    float m1 = 0.f, m3 = 0.f;
+    // P and Z with their decays; the scale of the token's k or q goes with the
+    // one that is summed over.  A block's rows are in one chunk, its columns too.
+    float m1 = 0.f, m2 = 0.f, m3 = 0.f;
     // Blocks of a second chunk that does not exist stay zero, as their rows of
     // the operands are: it has no decays to read.
     if (block_exists(mt, sb, nch)) {
@@ -499,13 +501,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
             float& z = Z[i][2 * hh + e];
             p *= a.scale * w;
             z = s < t ? z * (bt * w) : 0.f;
-            m1 = fmaxf(m1, fabsf(p)), m3 = fmaxf(m3, fabsf(z));
+            m1 = fmaxf(m1, fabsf(p * ik[s])), m2 = fmaxf(m2, fabsf(p * iq[t]));
+            m3 = fmaxf(m3, fmaxf(fabsf(z * ik[t]), fabsf(z * ik[s])));
           }
       }
     }
     {
-      const float m2 = absmax_bits(__float_as_uint(m1 * qt));
-      m1 = absmax_bits(__float_as_uint(m1 * ks)), m3 = absmax_bits(__float_as_uint(m3 * fmaxf(kt, ks)));
+      m1 = absmax_bits(__float_as_uint(m1)), m2 = absmax_bits(__float_as_uint(m2)), m3 = absmax_bits(__float_as_uint(m3));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) pi += __shfl_xor_sync(0xffffffffu, pi, o);
       if (lane == 0) wmax[0][warp] = m1, wmax[1][warp] = m2, wmax[2][warp] = m3, wpi[warp] = pi;
@@ -514,16 +516,18 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
     copy_states(h + 1, 0);
     float i1, i2, i3;
     {
-      m1 = lane < kGradWarps ? wmax[0][lane] : 0.f, m3 = lane < kGradWarps ? wmax[2][lane] : 0.f;
-      const float m2 = lane < kGradWarps ? wmax[1][lane] : 0.f;
+      m1 = lane < kGradWarps ? wmax[0][lane] : 0.f, m2 = lane < kGradWarps ? wmax[1][lane] : 0.f;
+      m3 = lane < kGradWarps ? wmax[2][lane] : 0.f;
       const float s1 = pow2_scale(absmax_bits(__float_as_uint(m1)), i1), s2 = pow2_scale(absmax_bits(__float_as_uint(m2)), i2),
                   s3 = pow2_scale(absmax_bits(__float_as_uint(m3)), i3);
       if (sb <= mt) {
-        const float f1 = ks * s1, f2 = qt * s2, fa = kt * s3, fb = ks * s3;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
+            const float kt = ik[r0 + 8 * hh], qt = iq[r0 + 8 * hh];
+            const float2 ks = *reinterpret_cast<const float2*>(ik + 16 * sb + 8 * i + 2 * (lane & 3));
+            const float2 p = make_float2(P[i][2 * hh], P[i][2 * hh + 1]), z = make_float2(Z[i][2 * hh], Z[i][2 * hh + 1]);
             const uint32_t o = tile_off<64>(r0 + 8 * hh, 16 * sb + 8 * i + 2 * (lane & 3));
             const auto put = [&](int at, float2 x) {
               uint32_t hi, lo;
@@ -531,10 +535,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
               *reinterpret_cast<uint32_t*>(sm + at + o) = hi;
               *reinterpret_cast<uint32_t*>(sm + at + G::kSmall + o) = lo;
             };
-            put(G::kW1, mul2(P[i][2 * hh], P[i][2 * hh + 1], f1));
-            put(G::kW2, mul2(P[i][2 * hh], P[i][2 * hh + 1], f2));
-            put(G::kZa, mul2(Z[i][2 * hh], Z[i][2 * hh + 1], fa));
-            put(G::kZb, mul2(Z[i][2 * hh], Z[i][2 * hh + 1], fb));
+            put(G::kW1, mul2(p.x * ks.x, p.y * ks.y, s1));
+            put(G::kW2, mul2(p.x * qt, p.y * qt, s2));
+            put(G::kZa, mul2(z.x * kt, z.y * kt, s3));
+            put(G::kZb, mul2(z.x * ks.x, z.y * ks.y, s3));
           }
       }
     }
@@ -572,7 +576,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
         q0 += __shfl_xor_sync(0xffffffffu, q0, o);
         q1 += __shfl_xor_sync(0xffffffffu, q1, o);
       }
-      if ((lane & 3) == 0) sums[2 + quarter][r0] = q0 * qt, sums[2 + quarter][r0 + 8] = q1 * qt;
+      if ((lane & 3) == 0) sums[2 + quarter][r0] = q0 * iq[r0], sums[2 + quarter][r0 + 8] = q1 * iq[r0 + 8];
       add_rows(dq, dqh, 1.f, 1.f);
     }
     __syncthreads();

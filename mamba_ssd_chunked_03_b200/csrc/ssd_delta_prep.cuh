@@ -37,7 +37,7 @@ namespace delta {
 constexpr int kPrepThreads = 128;
 constexpr int kGP = 36;  // row pitch of the fp32 32 x 32 tiles
 
-// Per-token factors of a chunk (the powers of two of the operand tiles are in them).
+// Per-token factors of a chunk (the powers of two of the operand tiles' rows are in them).
 struct alignas(16) Factors {
   float kc[kC];   // forward: exp(cs) / k scale;  reverse: exp(cs_C - cs) / k scale
   float qc[kC];   // scale exp(cs) / q scale
@@ -46,10 +46,8 @@ struct alignas(16) Factors {
   float mu[kC];   // 1 / scale of the rows of M
   float beta[kC];
   float whole;     // exp(cs_C)
-  float ik, iq;    // 1 / scale of the chunk's k and q tiles
   float norm;      // forward: a power of two that no row sum of the inverse's magnitudes exceeds
   float ucm, qcm;  // largest magnitudes of uc and qc
-  float pad[2];
 };
 
 // What the gradients need of a chunk's decays besides (kept beside the reverse
@@ -58,6 +56,7 @@ struct alignas(16) Decays {
   double cs[kC];               // cumulative log2 decay
   float into[kC], outof[kC];   // exp(cs), exp(cs_C - cs)
   float inv[kC];               // 1 / exp(cs), if `plain`
+  float ik[kC], iq[kC];        // 1 / scale of the rows of k and q
   int plain;                   // exp(cs_t - cs_s) is into_t inv_s
   int pad[3];
 };
@@ -147,7 +146,8 @@ __global__ void __launch_bounds__(kPrepThreads, NT * sizeof(T) <= 256 ? 6 : 3) k
   float* gq = gk + kC * kGP;
   char* const tiles = sm + 2 * kC * kGP * 4;                // k and q; when their products are formed,
   float* at = reinterpret_cast<float*>(tiles);              // a warp's A, transposed
-  __shared__ float maxes[2][kPrepThreads / 32];
+  __shared__ __align__(8) float iscale[2][kC];     // 1 / scale of the rows of k and q
+  __shared__ uint32_t parts[2][kC][2];         // of a row that lies across two warps
   __shared__ __align__(16) float col[kPrepThreads / 32][2][kC];
   __shared__ double css[kPrepThreads / 32][kC];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(kPrepThreads, NT * sizeof(T) <= 256 ? 6 : 3) k
   }
   if (c.n == 0) return;
   const uint32_t smu = sm100::smem_u32(tiles);
-  float inv_k, inv_q;
-  {  // the tiles of k and q: fp16, each scaled by its largest magnitude
+  // The tiles of k and q: fp16, each row scaled by its largest magnitude, so that
+  // a token's bits do not depend on the tokens beside it.
+  {
     const int row0 = threadIdx.x / PC, cc = (threadIdx.x % PC) * E;
     constexpr int kStep = kPrepThreads / PC;
     char* out = a.tokens + (ch * a.G + grp) * X::kBytes;
@@ -179,36 +180,42 @@ __global__ void __launch_bounds__(kPrepThreads, NT * sizeof(T) <= 256 ? 6 : 3) k
                                           : make_uint4(0, 0, 0, 0);
       }
     }
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int x = 0; x < V; ++x) {
-        const uint32_t u[4] = {raw[w][x].x, raw[w][x].y, raw[w][x].z, raw[w][x].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {  // the bits of magnitudes order as they do
-          if constexpr (sizeof(T) == 2) m = __vmaxu2(m, u[e] & 0x7fff7fffu);
-          else m = max(m, u[e] & 0x7fffffffu);
-        }
-      }
-      if constexpr (sizeof(T) == 2) m = max(m << 16, m & 0xffff0000u);
-      const float f = absmax_bits(m);
-      if (lane == 0) maxes[w][warp] = f;
-    }
-    __syncthreads();
-    float sc[2];
-    sc[0] = pow2_unit(fmaxf(fmaxf(maxes[0][0], maxes[0][1]), fmaxf(maxes[0][2], maxes[0][3])), inv_k);
-    sc[1] = pow2_unit(fmaxf(fmaxf(maxes[1][0], maxes[1][1]), fmaxf(maxes[1][2], maxes[1][3])), inv_q);
+    uint32_t most[2][V];  // a row's largest magnitude: the bits of magnitudes order as they do
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
       for (int x = 0; x < V; ++x) {
         const uint32_t u[4] = {raw[w][x].x, raw[w][x].y, raw[w][x].z, raw[w][x].w};
-        const uint32_t o = w * X::kTerms * X::kTile + tile_off<NT>(row0 + x * kStep, cc);
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (sizeof(T) == 2) m = __vmaxu2(m, u[e] & 0x7fff7fffu);
+          else m = max(m, u[e] & 0x7fffffffu);
+        }
+        if constexpr (sizeof(T) == 2) m = max(m << 16, m & 0xffff0000u);
+#pragma unroll
+        for (int o = 1; o < PC && o < 32; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if constexpr (PC > 32) {
+          if (lane == 0) parts[w][row0 + x * kStep][warp & 1] = m;
+        }
+        most[w][x] = m;
+      }
+    if constexpr (PC > 32) __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int x = 0; x < V; ++x) {
+        const int row = row0 + x * kStep;
+        if constexpr (PC > 32) most[w][x] = max(parts[w][row][0], parts[w][row][1]);
+        float inv;
+        const float sc = pow2_unit(__uint_as_float(most[w][x]), inv);
+        if (cc == 0) iscale[w][row] = inv;
+        const uint32_t u[4] = {raw[w][x].x, raw[w][x].y, raw[w][x].z, raw[w][x].w};
+        const uint32_t o = w * X::kTerms * X::kTile + tile_off<NT>(row, cc);
         if constexpr (sizeof(T) == 2) {
           uint32_t h[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = pack2(__fmul2_rn(bf16x2(u[e]), make_float2(sc[w], sc[w])));
+          for (int e = 0; e < 4; ++e) h[e] = pack2(__fmul2_rn(bf16x2(u[e]), make_float2(sc, sc)));
           const uint4 p = make_uint4(h[0], h[1], h[2], h[3]);
           *reinterpret_cast<uint4*>(tiles + o) = p;
           if (split == 0) *reinterpret_cast<uint4*>(out + o) = p;
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(kPrepThreads, NT * sizeof(T) <= 256 ? 6 : 3) k
           uint32_t hi[2], lo[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            split2(mul2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]), sc[w]), hi[e], lo[e]);
+            split2(mul2(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]), sc), hi[e], lo[e]);
           *reinterpret_cast<uint2*>(tiles + o) = make_uint2(hi[0], hi[1]);
           *reinterpret_cast<uint2*>(tiles + o + X::kTile) = make_uint2(lo[0], lo[1]);
           if (split == 0) {
@@ -256,17 +263,20 @@ __global__ void __launch_bounds__(kPrepThreads, NT * sizeof(T) <= 256 ? 6 : 3) k
         for (int n = 0; n < 4; ++n) mma(acc[n], A[1], B[0][n >> 1][2 * (n & 1)], B[0][n >> 1][2 * (n & 1) + 1]);
       }
     }
-    const float w0 = inv_k, w1 = isq ? inv_q : inv_k;
+    const float w0[2] = {iscale[isq][mt * 16 + (lane >> 2)], iscale[isq][mt * 16 + (lane >> 2) + 8]};
     float* dst = (isq ? gq : gk) + (mt * 16 + (lane >> 2)) * kGP + 2 * (lane & 3);
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < 4; ++n) {
+      const float2 w1 = *reinterpret_cast<const float2*>(iscale[0] + 8 * n + 2 * (lane & 3));
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh)
         *reinterpret_cast<float2*>(dst + 8 * hh * kGP + 8 * n) =
-            make_float2(acc[n][2 * hh] * w0 * w1, acc[n][2 * hh + 1] * w0 * w1);
+            make_float2(acc[n][2 * hh] * w0[hh] * w1.x, acc[n][2 * hh + 1] * w0[hh] * w1.y);
+    }
     __syncthreads();
   }
   at += warp * kC * kGP;
+  const float inv_k = iscale[0][lane], inv_q = iscale[1][lane];
   float* vb = col[warp][0];  // forward: beta / exp(cs);  reverse: 1 / exp(cs)
   double* cs = css[warp];
   const int64_t h1 = grp * a.hpg + ((int64_t)(split + 1) * a.heads < a.hpg ? (int64_t)(split + 1) * a.heads : a.hpg);
@@ -349,7 +359,7 @@ __global__ void __launch_bounds__(kPrepThreads, NT * sizeof(T) <= 256 ? 6 : 3) k
       f->kc[lane] = (rev ? outof : into) * inv_k;
       f->uc[lane] = uc;
       f->beta[lane] = bt;
-      if (lane == 31) f->whole = into, f->ik = inv_k, f->iq = inv_q, f->norm = norm, f->ucm = ucm, f->qcm = qcm;
+      if (lane == 31) f->whole = into, f->norm = norm, f->ucm = ucm, f->qcm = qcm;
       if (rev || kFwdM) {
         row(gq, a.scale, 0, [&](int cidx, float w) { t[cidx] = w; });
         char* mi = img + (rev ? HR::kM : HF::kM);
@@ -358,6 +368,7 @@ __global__ void __launch_bounds__(kPrepThreads, NT * sizeof(T) <= 256 ? 6 : 3) k
         if (rev) {
           Decays* d = reinterpret_cast<Decays*>(img + HR::kBytes);
           d->cs[lane] = sum, d->into[lane] = into, d->outof[lane] = outof, d->inv[lane] = inv;
+          d->ik[lane] = inv_k, d->iq[lane] = inv_q;
           if (lane == 0) d->plain = plain;
         }
       }

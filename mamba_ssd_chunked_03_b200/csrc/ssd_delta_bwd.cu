@@ -99,7 +99,7 @@ cudaError_t run_all(const ssd_delta_bwd_args* b, const Shape& s, const Layout& l
   GradArgs g = {};
   g.L = s.L, g.H = s.H, g.G = s.G, g.P = s.P, g.N = s.N, g.hpg = p.hpg;
   g.per_row = (int)((s.L + kCheck - 1) / kCheck), g.splits = l.splits, g.heads = l.heads, g.nslices = l.nslices;
-  g.pg = l.pg, g.scale = s.scale, g.tokens = p.tokens, g.head = p.rev, g.v = v, g.dy = dy, g.pv = pv, g.pe = w.pe;
+  g.pg = l.pg, g.scale = s.scale, g.tokens = p.tokens, g.head = p.rev, g.v = v, g.dy = dy, g.g = a->g, g.pv = pv, g.pe = w.pe;
   g.e = at(l.e), g.d = at(l.d), g.s = at(l.s), g.ds = at(l.ds), g.s_fin = b->dfinal_states ? at(l.s_fin) : nullptr;
   g.max_y = at(l.max_y), g.max_e = at(l.max_e), g.max_d = at(l.max_d), g.max_s = at(l.max_s), g.max_ds = at(l.max_ds);
   g.initial = a->initial_states != nullptr;

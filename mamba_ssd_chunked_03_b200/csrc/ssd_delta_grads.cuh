@@ -12,8 +12,10 @@
 // dg by the last line takes each token's pi_t = <G_t, S_t> from the next one's
 // (pi_{t-1} = dg_t + dy_{t-1}.y_{t-1}, dg_t = pi_t - dv_t.v_t, and dy.y = dq.q).
 // <dS, S> is known at both ends of the 64 tokens (dg_0 is that of the tokens
-// before), so the sums run from the nearer end, over 32 tokens at most, and
-// rounding does not pile up along the sequence.  All operands that are results
+// before), so the sums run from the nearer end, over 32 tokens at most (64 in a
+// row's first ones, where an initial state comes in), and rounding does not pile
+// up along the sequence.  It is relative to those sums' terms; where exp(g) is
+// zero, dg is zero and the sums start anew.  All operands that are results
 // are split in two terms: dg needs dq to fp32 accuracy, and what is returned is
 // rounded once.  (One term for dk's in bf16, errors of 2^-12 before its own
 // rounding: 354 us where it now takes 414.)
@@ -53,6 +55,7 @@ struct GradArgs {
   const char* head;    // RevTiles: factors and decays
   const void* v;
   const void* dy;
+  const float* g;
   const float* e;
   const float* d;
   const float* s;       // [slot][head][P][N] states that enter
@@ -632,9 +635,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
       }
 }
 
-// dg: a warp takes the 64 tokens of a slot and head, two a lane; the second
-// half from the end, the first half from the start (or, where an initial state
-// comes in, all of it from the end).
+// dg: a warp takes the 64 tokens of a slot and head, two a lane, each summed from
+// the nearer known end.  Known are <dS, S> at either end of the slot (not at the
+// start where an initial state comes in: up to 64 tokens are then summed), and
+// zero at a token whose decay is zero: nothing passes it in either direction, so
+// sums neither cross it nor carry their rounding to the other side.
 __global__ void __launch_bounds__(256) k_delta_dg(const GradArgs a, float* __restrict__ dg) {
   const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (i >= a.slots_n * a.H) return;
@@ -644,11 +649,13 @@ __global__ void __launch_bounds__(256) k_delta_dg(const GradArgs a, float* __res
   if (s.n == 0) return;
   const bool start = s.h0 == kInside || s.h0 < 0 || !a.initial;  // <dS, S> before the slot is known
   float x[2], before = 0.f, after = 0.f;  // tokens 2 lane, 2 lane + 1: dq.q - dv.v
+  bool z[2];                              // exp(g) is zero
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int t = 2 * lane + e;
     const int64_t o = ((int64_t)s.tok + t) * a.H + h;
     x[e] = t < s.n ? -a.dvv[o] : 0.f;
+    z[e] = t < s.n && expf(a.g[o]) == 0.f;
     if (t < s.n)
       for (int c = 0; c < a.nslices; ++c) x[e] += a.qdq[c * a.part_stride + o];
   }
@@ -656,22 +663,34 @@ __global__ void __launch_bounds__(256) k_delta_dg(const GradArgs a, float* __res
     after += a.pi[(c * a.slots_n + slot) * a.H + h];
     if (s.h0 == kInside) before += a.pi[(c * a.slots_n + slot - 1) * a.H + h];
   }
-  float up = x[0] + x[1], down = up;
+  const uint32_t m0 = __ballot_sync(0xffffffffu, z[0]), m1 = __ballot_sync(0xffffffffu, z[1]);
+  const bool zn = lane < 31 && ((m0 >> (lane + 1)) & 1);  // the token after this lane's two
+  // sums over the tokens before a lane's first since the last zero, and from it to the next one
+  float up = (z[1] ? 0.f : x[0]) + x[1], down = x[0] + (z[1] ? 0.f : x[1]);
+  bool cut_up = z[0] || z[1], cut_down = z[1] || zn;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const float u = __shfl_up_sync(0xffffffffu, up, o), d = __shfl_down_sync(0xffffffffu, down, o);
-    if (lane >= o) up += u;
-    if (lane + o < 32) down += d;
+    const int cu = __shfl_up_sync(0xffffffffu, (int)cut_up, o), cd = __shfl_down_sync(0xffffffffu, (int)cut_down, o);
+    if (lane >= o) up += cut_up ? 0.f : u, cut_up = cut_up || cu;
+    if (lane + o < 32) down += cut_down ? 0.f : d, cut_down = cut_down || cd;
   }
-  // sums over the tokens before this lane's, and from this lane's on
-  const float upto = __shfl_up_sync(0xffffffffu, up, 1), from = down;
-  const int mid = start ? (s.n + 1) / 2 : 0;
+  const float upto = __shfl_up_sync(0xffffffffu, up, 1), rest = __shfl_down_sync(0xffffffffu, down, 1);
+  const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int t = 2 * lane + e;
     if (t >= s.n) continue;
-    const float b = before - ((lane ? upto : 0.f) + (e ? x[0] : 0.f)), f = after + (e ? from - x[0] : from);
-    dg[((int64_t)s.tok + t) * a.H + h] = t < mid ? b : f;
+    // the last zero at or before t, the next one after it (-1, 64: none)
+    const uint32_t p0 = m0 & (below | 1u << lane), p1 = e ? m1 & (below | 1u << lane) : m1 & below;
+    const uint32_t q0 = m0 & ~(below | 1u << lane), q1 = e ? m1 & ~(below | 1u << lane) : m1 & ~below;
+    const int last = max(p0 ? 2 * (31 - __clz(p0)) : -1, p1 ? 2 * (31 - __clz(p1)) + 1 : -1);
+    const int next = min(q0 ? 2 * (__ffs(q0) - 1) : 64, q1 ? 2 * (__ffs(q1) - 1) + 1 : 64);
+    const float pre = (lane && !z[0] ? upto : 0.f), suf = e ? x[1] + (zn || lane == 31 ? 0.f : rest) : down;
+    const float b = (last < 0 ? before : 0.f) - (e ? (z[1] ? 0.f : pre + x[0]) : pre);
+    const float f = (next == 64 ? after : 0.f) + suf;
+    const int away = last >= 0 ? t - last : start ? t : 128, to = (next < 64 ? next : s.n) - t;
+    dg[((int64_t)s.tok + t) * a.H + h] = last == t ? 0.f : away <= to ? b : f;
   }
 }
 

@@ -7,7 +7,11 @@
 // Bound by HBM: every tensor is read once and every output written once.  A
 // row belongs to a group of GT threads (part of a warp, or a whole CTA), which
 // holds it in registers: the mean first, then the mean square of the
-// differences, so that a large mean costs no accuracy.  Groups walk the rows
+// differences to it, so that a large mean costs no accuracy.  In fp32 the
+// differences' own mean is taken out of them again: it is what the rounding of
+// the mean is off by.  In bf16 the sum of equal values is exact (8 bits each), so
+// a mean divided without error leaves zeros, and other rows deviate by more than
+// the mean's rounding shows.  Groups walk the rows
 // with a fixed stride and load the next row before they work on this one;
 // weights, biases and the sums of their gradients stay in registers all the
 // way.  The backward's partial sums (one set a CTA) are added by a second
@@ -42,7 +46,7 @@ struct Args {
   void* out;    // forward: y; backward: dx
   void* dz;
   float* part;  // backward: [2][CTAs][cols] partial sums of dw, db, or null
-  float* stat;  // wide rows: [rows][2] mean, rstd
+  float* stat;  // wide rows: [rows][3] mean, rstd, and what the mean's rounding takes off n
 };
 
 // Arithmetic on one value or on two at once (half the instructions).
@@ -210,6 +214,7 @@ template <typename T, int E, int GT, int VPL, int BT, int MINB, bool BWD, bool G
 __global__ void __launch_bounds__(BT, MINB) k_norm(const Args a) {
   using Pk = Pack<T, E>;
   constexpr int GC = GT > 32 ? 1 : kThreads / GT;  // groups of a CTA
+  constexpr bool kTwice = sizeof(T) == 4;          // the differences' mean is taken out too
   __shared__ float4 red[2][kMostThreads / 32];
   GroupSum<GT> sum{red};
   const int gt = GT > 32 ? blockDim.x : GT;  // threads of a row
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(BT, MINB) k_norm(const Args a) {
     const int64_t r = r0 + g;
     const bool live = r < a.rows;
     V x[VPL][EV], z[VPL][EV], d[VPL][EV];  // x - mean, the gate, and dout: then dout SiLU(z)
-    V s0 = all<V>(0.f), sq = all<V>(0.f);
+    V s0 = all<V>(0.f), s1 = all<V>(0.f), sq = all<V>(0.f);
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       xr[v].get(x[v]);
@@ -269,24 +274,33 @@ __global__ void __launch_bounds__(BT, MINB) k_norm(const Args a) {
     fetch(r + stride);
     float t[1] = {total(s0)};
     sum(t);
-    const float mean = t[0] * inv_cols;
+    float mean = t[0] * inv_cols;
+    if constexpr (!kTwice) mean = fmaf(fmaf(-mean, (float)cols, t[0]), inv_cols, mean);
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
 #pragma unroll
       for (int e = 0; e < EV; ++e) {
         x[v][e] = add(x[v][e], all<V>(col(v) < cols ? -mean : 0.f));
+        if constexpr (kTwice) s1 = add(s1, x[v][e]);
         sq = fma_(x[v][e], x[v][e], sq);
       }
-    t[0] = total(sq);
-    sum(t);
-    const float rstd = live ? 1.f / sqrtf(fmaf(t[0], inv_cols, a.eps)) : 0.f;
+    float u[kTwice ? 2 : 1] = {total(sq)}, dm = 0.f;
+    if constexpr (kTwice) u[1] = total(s1);
+    sum(u);
+    if constexpr (kTwice) dm = u[1] * inv_cols;
+    const float rstd = live ? 1.f / sqrtf(fmaxf(fmaf(u[0], inv_cols, -dm * dm), 0.f) + a.eps) : 0.f;
+    const V scale = all<V>(rstd), shift = all<V>(-dm * rstd);
+    const auto normed = [&](V c) {
+      if constexpr (kTwice) return fma_(c, scale, shift);
+      else return mul(c, scale);
+    };
     if constexpr (!BWD) {
 #pragma unroll
       for (int v = 0; v < VPL; ++v) {
         V y[EV];
 #pragma unroll
         for (int e = 0; e < EV; ++e) {
-          y[e] = fma_(mul(x[v][e], all<V>(rstd)), w[v][e], b[v][e]);
+          y[e] = fma_(normed(x[v][e]), w[v][e], b[v][e]);
           if constexpr (GATE) y[e] = mul(y[e], silu<T>(z[v][e]));
         }
         if (live && col(v) < cols) Pk::store(static_cast<T*>(a.out) + r * cols + col(v), y);
@@ -298,7 +312,7 @@ __global__ void __launch_bounds__(BT, MINB) k_norm(const Args a) {
         V dz[EV];
 #pragma unroll
         for (int e = 0; e < EV; ++e) {
-          x[v][e] = mul(x[v][e], all<V>(rstd));
+          x[v][e] = normed(x[v][e]);
           V h = d[v][e];
           if constexpr (GATE) {  // SiLU' = s + z s (1 - s)
             const V zb = bounded(z[v][e]), sg = sigmoid<T>(zb), zs = mul(zb, sg);
@@ -529,7 +543,7 @@ __global__ void __launch_bounds__(BT, MINB) k_norm_row(const Args a) {
     for (int q = 0; q < NR; ++q) {
       const int64_t r = r0 + (int64_t)q * gridDim.x;
       if (r >= a.rows) continue;
-      const float dm = t[q][0] * inv_cols, mean = K[q] + dm;
+      const float dm = t[q][0] * inv_cols;
       const float rstd = 1.f / sqrtf(fmaxf(fmaf(t[q][1], inv_cols, -dm * dm), 0.f) + a.eps);
       float m1 = 0.f, m2 = 0.f;
       if constexpr (BWD) m1 = t[q][2] * inv_cols, m2 = rstd * (t[q][3] - dm * t[q][2]) * inv_cols;
@@ -544,7 +558,7 @@ __global__ void __launch_bounds__(BT, MINB) k_norm_row(const Args a) {
         if constexpr (GATE || !BWD) weights(cols + col(v), b);
 #pragma unroll
         for (int e = 0; e < EV; ++e) {
-          const V n = mul(add(x[e], all<V>(-mean)), all<V>(rstd));
+          const V n = fma_(add(x[e], all<V>(-K[q])), all<V>(rstd), all<V>(-dm * rstd));
           if constexpr (!BWD) {
             x[e] = fma_(n, w[e], b[e]);
             if constexpr (GATE) x[e] = mul(x[e], silu<T>(z[e]));
@@ -590,20 +604,21 @@ __global__ void __launch_bounds__(kThreads) k_norm_wide(const Args a) {
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * cols;
     const T* z = a.z ? static_cast<const T*>(a.z) + r * cols : nullptr;
-    float s[1] = {0.f}, q[1] = {0.f};
+    float s[1] = {0.f}, q[2] = {0.f, 0.f};
     for (int64_t c = threadIdx.x; c < cols; c += kThreads) s[0] += to_f(x[c]);
     sum(s);
     const float mean = s[0] / (float)cols;
     for (int64_t c = threadIdx.x; c < cols; c += kThreads) {
       const float d = to_f(x[c]) - mean;
-      q[0] = fmaf(d, d, q[0]);
+      q[0] += d, q[1] = fmaf(d, d, q[1]);
     }
     sum(q);
-    const float rstd = 1.f / sqrtf(q[0] / (float)cols + a.eps);
+    const float dm = q[0] / (float)cols;
+    const float rstd = 1.f / sqrtf(fmaxf(q[1] / (float)cols - dm * dm, 0.f) + a.eps), shift = -dm * rstd;
     if constexpr (!BWD) {
       T* y = static_cast<T*>(a.out) + r * cols;
       for (int64_t c = threadIdx.x; c < cols; c += kThreads) {
-        float v = fmaf((to_f(x[c]) - mean) * rstd, a.w ? a.w[c] : 1.f, a.b ? a.b[c] : 0.f);
+        float v = fmaf(fmaf(to_f(x[c]) - mean, rstd, shift), a.w ? a.w[c] : 1.f, a.b ? a.b[c] : 0.f);
         if (z) v *= silu<T>(to_f(z[c]));
         put(y + c, v);
       }
@@ -611,7 +626,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_wide(const Args a) {
       const T* dout = static_cast<const T*>(a.dout) + r * cols;
       float m[2] = {0.f, 0.f};
       for (int64_t c = threadIdx.x; c < cols; c += kThreads) {
-        const float n = (to_f(x[c]) - mean) * rstd;
+        const float n = fmaf(to_f(x[c]) - mean, rstd, shift);
         float h = to_f(dout[c]);
         const float w = a.w ? a.w[c] : 1.f;
         if (z) {
@@ -625,10 +640,10 @@ __global__ void __launch_bounds__(kThreads) k_norm_wide(const Args a) {
       }
       sum(m);
       const float m1 = m[0] / (float)cols, m2 = m[1] / (float)cols;
-      if (threadIdx.x == 0) a.stat[2 * r] = mean, a.stat[2 * r + 1] = rstd;
+      if (threadIdx.x == 0) a.stat[3 * r] = mean, a.stat[3 * r + 1] = rstd, a.stat[3 * r + 2] = shift;
       T* dx = static_cast<T*>(a.out) + r * cols;
       for (int64_t c = threadIdx.x; c < cols; c += kThreads) {
-        const float n = (to_f(x[c]) - mean) * rstd;
+        const float n = fmaf(to_f(x[c]) - mean, rstd, shift);
         float h = to_f(dout[c]);
         if (z) h *= silu<T>(to_f(z[c]));
         put(dx + c, rstd * (h * (a.w ? a.w[c] : 1.f) - m1 - n * m2));
@@ -645,7 +660,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_wide_cols(const Args a) {
   if (c >= cols) return;
   float dw = 0.f, db = 0.f;
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
-    const float n = (to_f(static_cast<const T*>(a.x)[r * cols + c]) - a.stat[2 * r]) * a.stat[2 * r + 1];
+    const float n = fmaf(to_f(static_cast<const T*>(a.x)[r * cols + c]) - a.stat[3 * r], a.stat[3 * r + 1], a.stat[3 * r + 2]);
     float h = to_f(static_cast<const T*>(a.dout)[r * cols + c]);
     if (a.z) h *= silu<T>(to_f(static_cast<const T*>(a.z)[r * cols + c]));
     dw = fmaf(h, n, dw);
@@ -787,7 +802,7 @@ size_t part_bytes(int64_t cols) {
   const size_t a = (size_t)kParts * (size_t)cols, b = (size_t)kSMs * kRowParts;
   return align_up(2 * (a > b ? a : b) * 4, kWsAlign);
 }
-size_t bwd_workspace(int64_t rows, int64_t cols) { return part_bytes(cols) + align_up((size_t)rows * 8, kWsAlign); }
+size_t bwd_workspace(int64_t rows, int64_t cols) { return part_bytes(cols) + align_up((size_t)rows * 12, kWsAlign); }
 
 }  // namespace
 }  // namespace ssd

@@ -665,7 +665,8 @@ typedef struct {
 } ssd_norm_bwd_args;
 
 /* Workspace bytes ssd_layer_norm_bwd needs (rows and cols only), or 0 if the
- * sizes are invalid. */
+ * sizes are invalid: 8 rows cols, but no more than 19.4 MB or 3552 cols,
+ * whichever is larger; and 12 rows where cols is above 4096. */
 SSD_API size_t ssd_layer_norm_bwd_workspace_size(const ssd_norm_bwd_args* args);
 
 SSD_API ssd_status ssd_layer_norm_bwd(const ssd_norm_bwd_args* args, void* stream);

@@ -797,12 +797,16 @@ ssd_status check(int64_t rows, int64_t cols, ssd_dtype dtype, float eps) {
   return SSD_OK;
 }
 
-// Partial sums, then the statistics of rows that are swept from memory.
-size_t part_bytes(int64_t cols) {
-  const size_t a = (size_t)kParts * (size_t)cols, b = (size_t)kSMs * kRowParts;
-  return align_up(2 * (a > b ? a : b) * 4, kWsAlign);
+// Partial sums, one set for each CTA (no more of them than rows), then the
+// statistics of rows that are swept from memory: none of up to 4096 columns is,
+// wherever they start.
+size_t part_bytes(int64_t rows, int64_t cols) {
+  const int64_t grid = kParts * cols, row = (int64_t)kSMs * kRowParts, all = rows * cols, most = grid > row ? grid : row;
+  return align_up((size_t)(all < most ? all : most) * 2 * 4, kWsAlign);
 }
-size_t bwd_workspace(int64_t rows, int64_t cols) { return part_bytes(cols) + align_up((size_t)rows * 12, kWsAlign); }
+size_t bwd_workspace(int64_t rows, int64_t cols) {
+  return part_bytes(rows, cols) + (cols > 4096 ? align_up((size_t)rows * 12, kWsAlign) : 0);
+}
 
 }  // namespace
 }  // namespace ssd
@@ -851,7 +855,7 @@ extern "C" SSD_API ssd_status ssd_layer_norm_bwd(const ssd_norm_bwd_args* a, voi
   float* part = static_cast<float*>(a->workspace);
   const bool sums = a->dweight || a->dbias;
   k.part = sums ? part : nullptr;
-  k.stat = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + part_bytes(a->cols));
+  k.stat = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + part_bytes(a->rows, a->cols));
   const auto all_at = [&](size_t n) {
     bool is = a->cols * esz % n == 0;
     for (const void* p : {a->x, a->dout, (const void*)a->dx, a->z, (const void*)a->dz}) is = is && aligned(p, n);

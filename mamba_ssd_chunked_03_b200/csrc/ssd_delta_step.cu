@@ -121,13 +121,14 @@ __global__ void __launch_bounds__(kThreads) k_delta_step(const Args a) {
 
 template <typename T, int LP, int NK>
 cudaError_t launch(Args& a, int64_t units, cudaStream_t st) {
-  // Few rows: two a lane instead of eight, so that four times the CTAs share the loads.
+  // Few rows: two a lane instead of eight, so that four times the CTAs share the
+  // loads (of the small variant at most 4 x 2 x 148; of the other a CTA takes 16
+  // rows or more, which bounds the grid before the launch).
   constexpr int kFew = 2, kMany = NK == 1 ? 8 : 4;
   const int64_t few = (int64_t)(32 / LP) * kFew * (kThreads / 32), many = few / kFew * kMany;
   const bool small = units * ((a.P + many - 1) / many) < 2 * 148;
   const int64_t cta = small ? few : many;
   a.slices = (int)((a.P + cta - 1) / cta);
-  if ((double)units * a.slices >= 2147483647.0) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)(units * a.slices);
   if (small) k_delta_step<T, LP, NK, kFew><<<grid, kThreads, 0, st>>>(a);
   else k_delta_step<T, LP, NK, kMany><<<grid, kThreads, 0, st>>>(a);
@@ -159,7 +160,7 @@ extern "C" SSD_API ssd_status ssd_delta_step(const ssd_delta_step_args* a, void*
   const size_t esz = a->dtype == SSD_BF16 ? 2 : 4;
   if (!aligned(a->state, 16) || !aligned(a->q, 4 * esz) || !aligned(a->k, 4 * esz)) return SSD_ERR_INVALID_ARG;
   if (a->dstate % 4 != 0 || a->dstate > kMaxN || a->headdim > 65536) return SSD_ERR_UNSUPPORTED;
-  // a CTA takes 16 rows at least: the grid stays below 2^31
+  // a CTA takes 16 rows at least where the grid is large: it stays below 2^31
   if ((double)a->batch * (double)a->nheads * (double)((a->headdim + 15) / 16) >= 2147483647.0)
     return SSD_ERR_UNSUPPORTED;
   Args s;

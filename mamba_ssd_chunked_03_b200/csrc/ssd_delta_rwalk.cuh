@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_rwalk(con
   const char* head = a.heads + (run.chunk * a.H + h) * Hd::kStride;
   const T* v = static_cast<const T*>(a.v) + (run.tok * a.H + h) * a.pv + p_cta;
   float S[NT / 8][4];
-  if (a.s0 && run.fin >= 0) {
+  if (a.s0 && run.fin >= 0 && nc > 0) {
     load_state<NT>(S, a.s0 + (((int64_t)run.fin * a.H + h) * a.P + p0) * a.N, a.N, rows, lane);
   } else {
 #pragma unroll

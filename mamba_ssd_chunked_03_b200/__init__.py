@@ -921,12 +921,13 @@ def delta_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
               dy: torch.Tensor, scale: Optional[float] = None, initial_states: Optional[torch.Tensor] = None,
               seq_idx: Optional[torch.Tensor] = None, num_seqs: Optional[int] = None,
               dfinal_states: Optional[torch.Tensor] = None, want_dinitial_states: Optional[bool] = None,
-              workspace: Optional[torch.Tensor] = None) -> dict:
+              workspace: Optional[torch.Tensor] = None, check_seq: bool = False) -> dict:
     """The backward of ``delta_fwd`` via ``ssd_delta_bwd``: gradients of a loss
     given dy = dLoss/dy (like v) and dfinal_states = dLoss/dfinal_states (like
     final_states, also with seq_idx, or None).  Returns a dict: dq, dk and dv
     in their inputs' dtype, dg, dbeta and dinitial_states (by default only
-    when initial_states is given, else None) fp32."""
+    when initial_states is given, else None) fp32.  ``check_seq`` as for
+    ``delta_fwd``."""
     _check_delta(q, k, v, g, beta, initial_states, seq_idx)
     b, L, H, P = v.shape
     N = q.shape[3]
@@ -945,7 +946,8 @@ def delta_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
          "dbeta": torch.empty_like(beta),
          "dinitial_states": torch.empty(b, H, P, N, device=v.device, dtype=torch.float32)
          if want_dinitial_states else None}
-    a = DeltaBwdArgs(_delta_args(q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs), dy.data_ptr(),
+    a = DeltaBwdArgs(_delta_args(q, k, v, g, beta, scale, initial_states, seq_idx, num_seqs,
+                                 SSD_FLAG_CHECK_SEQ if check_seq else 0), dy.data_ptr(),
                      _ptr(dfinal_states), *(_ptr(t) for t in d.values()))
     need = int(lib.ssd_delta_bwd_workspace_size(a))
     if need:

@@ -513,7 +513,9 @@ SSD_API ssd_status ssd_bwd(const ssd_bwd_args* args, void* stream);
  * dstate up to 256 and any headdim up to 65536, batch * seqlen below 2^31.
  * q, k and the output are accessed 16 bytes at a time where they start on
  * 16-byte boundaries and their rows are multiples of 16 bytes, else element by
- * element; v and dy that are not so placed are copied to rows that are. */
+ * element; v and dy that are not so placed are copied to rows that are.  Every
+ * tensor starts on a boundary of its elements (else SSD_ERR_INVALID_ARG), here
+ * and in the entry points below. */
 typedef struct {
   int64_t batch, seqlen, nheads, headdim, dstate, ngroups;
   ssd_dtype dtype;             /* of q, k, v and y                               */

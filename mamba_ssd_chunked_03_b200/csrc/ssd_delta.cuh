@@ -198,6 +198,12 @@ cudaError_t launch_runs(const Shape& s, const int32_t* seq, const RunList& r, cu
 ssd_status resolve(const ssd_delta_args* a, Shape* s);
 
 inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+// Whether the inputs start on boundaries of their elements (an access elsewhere faults).
+inline bool inputs_aligned(const ssd_delta_args* a) {
+  const size_t esz = a->dtype == SSD_BF16 ? 2 : 4;
+  return aligned(a->q, esz) && aligned(a->k, esz) && aligned(a->v, esz) && aligned(a->g, 4) && aligned(a->beta, 4) &&
+         aligned(a->initial_states, 4) && aligned(a->seq_idx, 4);
+}
 
 }  // namespace delta
 }  // namespace ssd

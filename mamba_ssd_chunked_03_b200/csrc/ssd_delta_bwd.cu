@@ -126,6 +126,10 @@ extern "C" SSD_API ssd_status ssd_delta_bwd(const ssd_delta_bwd_args* b, void* s
   if (c != SSD_OK) return c;
   if (!a->q || !a->k || !a->v || !a->g || !a->beta || !b->dy || !b->dq || !b->dk || !b->dv || !b->dg || !b->dbeta)
     return SSD_ERR_INVALID_ARG;
+  const size_t esz = s.bf16 ? 2 : 4;
+  if (!inputs_aligned(a) || !aligned(b->dy, esz) || !aligned(b->dq, esz) || !aligned(b->dk, esz) || !aligned(b->dv, esz) ||
+      !aligned(b->dg, 4) || !aligned(b->dbeta, 4) || !aligned(b->dfinal_states, 4) || !aligned(b->dinitial_states, 4))
+    return SSD_ERR_INVALID_ARG;
   const Layout l = layout(s, b);
   if ((double)s.slots * s.G * l.nslices * l.splits >= 2147483647.0) return SSD_ERR_UNSUPPORTED;
   if (!b->workspace || b->workspace_bytes < l.total) return SSD_ERR_WORKSPACE;

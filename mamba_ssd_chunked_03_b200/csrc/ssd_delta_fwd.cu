@@ -26,6 +26,7 @@ extern "C" SSD_API ssd_status ssd_delta_fwd(const ssd_delta_args* a, void* strea
   const ssd_status st = resolve(a, &s);
   if (st != SSD_OK) return st;
   if (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->y) return SSD_ERR_INVALID_ARG;
+  if (!inputs_aligned(a) || !aligned(a->y, s.bf16 ? 2 : 4) || !aligned(a->final_states, 4)) return SSD_ERR_INVALID_ARG;
   const size_t need = ssd_delta_fwd_workspace_size(a);
   if (!a->workspace || a->workspace_bytes < need) return SSD_ERR_WORKSPACE;
   if (!aligned(a->workspace, kWsAlign)) return SSD_ERR_INVALID_ARG;

@@ -158,7 +158,9 @@ extern "C" SSD_API ssd_status ssd_delta_step(const ssd_delta_step_args* a, void*
   if (a->dtype != SSD_F32 && a->dtype != SSD_BF16) return SSD_ERR_INVALID_ARG;
   if (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->state || !a->y) return SSD_ERR_INVALID_ARG;
   const size_t esz = a->dtype == SSD_BF16 ? 2 : 4;
-  if (!aligned(a->state, 16) || !aligned(a->q, 4 * esz) || !aligned(a->k, 4 * esz)) return SSD_ERR_INVALID_ARG;
+  if (!aligned(a->state, 16) || !aligned(a->q, 4 * esz) || !aligned(a->k, 4 * esz) || !aligned(a->v, esz) ||
+      !aligned(a->y, esz) || !aligned(a->g, 4) || !aligned(a->beta, 4))
+    return SSD_ERR_INVALID_ARG;
   if (a->dstate % 4 != 0 || a->dstate > kMaxN || a->headdim > 65536) return SSD_ERR_UNSUPPORTED;
   // a CTA takes 16 rows at least where the grid is large: it stays below 2^31
   if ((double)a->batch * (double)a->nheads * (double)((a->headdim + 15) / 16) >= 2147483647.0)

@@ -819,7 +819,8 @@ extern "C" SSD_API ssd_status ssd_layer_norm(const ssd_norm_args* a, void* strea
   if (c != SSD_OK) return c;
   if (!a->x || !a->out) return SSD_ERR_INVALID_ARG;
   const size_t esz = a->dtype == SSD_BF16 ? 2 : 4;
-  if (!aligned(a->x, esz) || !aligned(a->out, esz) || !aligned(a->z, esz)) return SSD_ERR_INVALID_ARG;
+  if (!aligned(a->x, esz) || !aligned(a->out, esz) || !aligned(a->z, esz) || !aligned(a->weight, 4) || !aligned(a->bias, 4))
+    return SSD_ERR_INVALID_ARG;
   Args k = {};
   k.rows = a->rows, k.cols = a->cols, k.eps = a->eps;
   k.x = a->x, k.w = a->weight, k.b = a->bias, k.z = a->z, k.out = a->out;
@@ -847,6 +848,8 @@ extern "C" SSD_API ssd_status ssd_layer_norm_bwd(const ssd_norm_bwd_args* a, voi
   const size_t esz = a->dtype == SSD_BF16 ? 2 : 4, need = bwd_workspace(a->rows, a->cols);
   for (const void* p : {a->x, a->dout, (const void*)a->dx, a->z, (const void*)a->dz})
     if (!aligned(p, esz)) return SSD_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)a->weight, (const void*)a->bias, (const void*)a->dweight, (const void*)a->dbias})
+    if (!aligned(p, 4)) return SSD_ERR_INVALID_ARG;
   if (!a->workspace || a->workspace_bytes < need) return SSD_ERR_WORKSPACE;
   if (!aligned(a->workspace, kWsAlign)) return SSD_ERR_INVALID_ARG;
   Args k = {};

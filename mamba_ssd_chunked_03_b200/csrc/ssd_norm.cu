@@ -177,6 +177,10 @@ __device__ __forceinline__ float silu(float v) {
 template <typename T>
 __device__ __forceinline__ float2 silu(float2 v) { return make_float2(silu<T>(v.x), silu<T>(v.y)); }
 
+// (var + eps)^-1/2, for a variance that rounding may have taken below zero.  NaN
+// stays NaN, so that a row with an infinity or a NaN is NaN throughout.
+__device__ __forceinline__ float inv_dev(float var, float eps) { return 1.f / sqrtf((var < 0.f ? 0.f : var) + eps); }
+
 // Sums of N values over the GT threads of a group (GT > 32: the CTA's threads,
 // however many), the same bits in each of them.
 template <int GT>
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(BT, MINB) k_norm(const Args a) {
     if constexpr (kTwice) u[1] = total(s1);
     sum(u);
     if constexpr (kTwice) dm = u[1] * inv_cols;
-    const float rstd = live ? 1.f / sqrtf(fmaxf(fmaf(u[0], inv_cols, -dm * dm), 0.f) + a.eps) : 0.f;
+    const float rstd = live ? inv_dev(fmaf(u[0], inv_cols, -dm * dm), a.eps) : 0.f;
     const V scale = all<V>(rstd), shift = all<V>(-dm * rstd);
     const auto normed = [&](V c) {
       if constexpr (kTwice) return fma_(c, scale, shift);
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(BT, MINB) k_norm_row(const Args a) {
       const int64_t r = r0 + (int64_t)q * gridDim.x;
       if (r >= a.rows) continue;
       const float dm = t[q][0] * inv_cols;
-      const float rstd = 1.f / sqrtf(fmaxf(fmaf(t[q][1], inv_cols, -dm * dm), 0.f) + a.eps);
+      const float rstd = inv_dev(fmaf(t[q][1], inv_cols, -dm * dm), a.eps);
       float m1 = 0.f, m2 = 0.f;
       if constexpr (BWD) m1 = t[q][2] * inv_cols, m2 = rstd * (t[q][3] - dm * t[q][2]) * inv_cols;
 #pragma unroll
@@ -614,7 +618,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_wide(const Args a) {
     }
     sum(q);
     const float dm = q[0] / (float)cols;
-    const float rstd = 1.f / sqrtf(fmaxf(q[1] / (float)cols - dm * dm, 0.f) + a.eps), shift = -dm * rstd;
+    const float rstd = inv_dev(q[1] / (float)cols - dm * dm, a.eps), shift = -dm * rstd;
     if constexpr (!BWD) {
       T* y = static_cast<T*>(a.out) + r * cols;
       for (int64_t c = threadIdx.x; c < cols; c += kThreads) {

@@ -586,7 +586,7 @@ SSD_API ssd_status ssd_delta_step(const ssd_delta_step_args* args, void* stream)
  *
  * The states are recomputed from the inputs; what the forward returned is not
  * read.  A gradient has its input's type, rounded once: dq, dk and dv dtype,
- * the others fp32.  dg is formed from sums of dq.q - dv.v over up to 64 tokens
+ * the others fp32.  dg is formed from sums of dq.q - dv.v over up to 32 tokens
  * of a head, and rounded relative to their terms; it is zero where exp(g) is.
  * Every sum is taken in a fixed order, so results are
  * deterministic.  Unlike ssd_bwd, gradients of per-sequence final states are

@@ -12,7 +12,7 @@ using namespace ssd::delta;
 namespace {
 
 struct Layout {
-  size_t runs, tokens, fwd, rev, e, d, s, ds, s_fin, max_y, max_e, max_d, max_s, max_ds, part, qdq, dvv, pi, v, dy, total;
+  size_t runs, tokens, fwd, rev, e, d, s, ds, s_fin, max_y, max_e, max_d, max_s, max_ds, part, qdq, dvv, pi, dot, v, dy, total;
   int nslices, splits, heads, pg;
 };
 
@@ -52,6 +52,7 @@ Layout layout(const Shape& s, const ssd_delta_bwd_args* b) {
   l.qdq = take((size_t)l.nslices * tokens * s.H * 4);
   l.dvv = take(tokens * s.H * 4);
   l.pi = take((size_t)l.nslices * s.slots * s.H * 4);
+  l.dot = take((size_t)s.b * s.H * l.pg * 4);
   l.v = take(pad_bytes(s, b->fwd.v));
   l.dy = take(pad_bytes(s, b->dy));
   l.total = at;
@@ -93,7 +94,7 @@ cudaError_t run_all(const ssd_delta_bwd_args* b, const Shape& s, const Layout& l
   if ((e = launch_walk<T, kStates>(w, st)) != cudaSuccess) return e;
   w.heads = p.rev, w.v = dy, w.s0 = b->dfinal_states, w.out = b->dv, w.out_f = at(l.d);
   w.max_v = at(l.max_y), w.max_out = at(l.max_d), w.check = at(l.ds), w.max_check = at(l.max_ds);
-  w.fin = b->dinitial_states;
+  w.fin = b->dinitial_states, w.h0 = a->initial_states, w.dot = at(l.dot);
   w.out_vec = s.P * esz % 16 == 0 && aligned(b->dv, 16);
   if ((e = launch_rwalk<T>(w, st)) != cudaSuccess) return e;
   GradArgs g = {};
@@ -102,7 +103,7 @@ cudaError_t run_all(const ssd_delta_bwd_args* b, const Shape& s, const Layout& l
   g.pg = l.pg, g.scale = s.scale, g.tokens = p.tokens, g.head = p.rev, g.v = v, g.dy = dy, g.g = a->g, g.pv = pv, g.pe = w.pe;
   g.e = at(l.e), g.d = at(l.d), g.s = at(l.s), g.ds = at(l.ds), g.s_fin = b->dfinal_states ? at(l.s_fin) : nullptr;
   g.max_y = at(l.max_y), g.max_e = at(l.max_e), g.max_d = at(l.max_d), g.max_s = at(l.max_s), g.max_ds = at(l.max_ds);
-  g.initial = a->initial_states != nullptr;
+  g.dot = a->initial_states ? at(l.dot) : nullptr;
   g.slots = runs.slots, g.slots_n = s.slots, g.dq = b->dq, g.dk = b->dk;
   g.part = at(l.part), g.part_size = s.b * s.L * s.G * s.N;
   g.qdq = at(l.qdq), g.part_stride = s.b * s.L * s.H, g.dvv = at(l.dvv), g.pi = at(l.pi), g.dbeta = b->dbeta;

@@ -12,9 +12,9 @@
 // dg by the last line takes each token's pi_t = <G_t, S_t> from the next one's
 // (pi_{t-1} = dg_t + dy_{t-1}.y_{t-1}, dg_t = pi_t - dv_t.v_t, and dy.y = dq.q).
 // <dS, S> is known at both ends of the 64 tokens (dg_0 is that of the tokens
-// before), so the sums run from the nearer end, over 32 tokens at most (64 in a
-// row's first ones, where an initial state comes in), and rounding does not pile
-// up along the sequence.  It is relative to those sums' terms; where exp(g) is
+// before; at a row's start <dS, S> of the initial state, from the reverse walk), so
+// the sums run from the nearer end, over 32 tokens at most, and rounding does not
+// pile up along the sequence.  It is relative to those sums' terms; where exp(g) is
 // zero, dg is zero and the sums start anew.  All operands that are results
 // are split in two terms: dg needs dq to fp32 accuracy, and what is returned is
 // rounded once.  (One term for dk's in bf16, errors of 2^-12 before its own
@@ -74,7 +74,7 @@ struct GradArgs {
   float* dbeta;
   int64_t slots_n;
   int64_t pv, pe;       // row pitches of v and dy, and of e and d: multiples of four
-  bool initial;         // there are initial states
+  const float* dot;     // [row][head][pg] <gradient, initial state>, or null: there is none
   int pair;             // dq and dk can be written by twos
 };
 
@@ -636,9 +636,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
 }
 
 // dg: a warp takes the 64 tokens of a slot and head, two a lane, each summed from
-// the nearer known end.  Known are <dS, S> at either end of the slot (not at the
-// start where an initial state comes in: up to 64 tokens are then summed), and
-// zero at a token whose decay is zero: nothing passes it in either direction, so
+// the nearer known end.  Known are <dS, S> at either end of the slot, and zero at a
+// token whose decay is zero: nothing passes it in either direction, so
 // sums neither cross it nor carry their rounding to the other side.
 __global__ void __launch_bounds__(256) k_delta_dg(const GradArgs a, float* __restrict__ dg) {
   const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -647,7 +646,6 @@ __global__ void __launch_bounds__(256) k_delta_dg(const GradArgs a, float* __res
   const int64_t slot = i / a.H, h = i % a.H;
   const Slot s = a.slots ? a.slots[slot] : row_slot(a, slot);
   if (s.n == 0) return;
-  const bool start = s.h0 == kInside || s.h0 < 0 || !a.initial;  // <dS, S> before the slot is known
   float x[2], before = 0.f, after = 0.f;  // tokens 2 lane, 2 lane + 1: dq.q - dv.v
   bool z[2];                              // exp(g) is zero
 #pragma unroll
@@ -662,6 +660,11 @@ __global__ void __launch_bounds__(256) k_delta_dg(const GradArgs a, float* __res
   for (int c = 0; c < a.nslices; ++c) {
     after += a.pi[(c * a.slots_n + slot) * a.H + h];
     if (s.h0 == kInside) before += a.pi[(c * a.slots_n + slot - 1) * a.H + h];
+  }
+  if (a.dot && s.h0 >= 0) {  // 16 rows of headdim a part: in a fixed order
+    for (int c = lane; c < a.pg; c += 32) before += a.dot[((int64_t)s.h0 * a.H + h) * a.pg + c];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   }
   const uint32_t m0 = __ballot_sync(0xffffffffu, z[0]), m1 = __ballot_sync(0xffffffffu, z[1]);
   const bool zn = lane < 31 && ((m0 >> (lane + 1)) & 1);  // the token after this lane's two
@@ -689,7 +692,7 @@ __global__ void __launch_bounds__(256) k_delta_dg(const GradArgs a, float* __res
     const float pre = (lane && !z[0] ? upto : 0.f), suf = e ? x[1] + (zn || lane == 31 ? 0.f : rest) : down;
     const float b = (last < 0 ? before : 0.f) - (e ? (z[1] ? 0.f : pre + x[0]) : pre);
     const float f = (next == 64 ? after : 0.f) + suf;
-    const int away = last >= 0 ? t - last : start ? t : 128, to = (next < 64 ? next : s.n) - t;
+    const int away = last >= 0 ? t - last : t, to = (next < 64 ? next : s.n) - t;
     dg[((int64_t)s.tok + t) * a.H + h] = last == t ? 0.f : away <= to ? b : f;
   }
 }

@@ -18,7 +18,7 @@
 // zero, dg is zero and the sums start anew.  All operands that are results
 // are split in two terms: dg needs dq to fp32 accuracy, and what is returned is
 // rounded once.  (One term for dk's in bf16, errors of 2^-12 before its own
-// rounding: 354 us where it now takes 414.)
+// rounding: 354 us where it now takes 400.)
 //
 // One CTA takes 64 tokens of a group, a slice of the columns n, and some of the
 // group's heads, whose dq and dk it adds in registers in a fixed order; sixteen
@@ -26,12 +26,12 @@
 // twice the columns each took 1.24 times as long: between its barriers a warp's
 // instructions depend on one another, and two warps a scheduler do not fill it.)
 //
-// b4 L2048 H32 G8 P64 N128: 414 us, 543 MB from HBM (1.3 TB/s).  Bound by
-// latency between its barriers: the tiles of a head take 220 KB, so one CTA an
-// SM, whose sixteen warps issue in 42 % of the clocks and keep the matrix pipe
-// busy for 18 %; what waits is fixed latencies (1.7 clocks an instruction),
-// shared memory (1.6), global loads of the state that leaves (1.3) and
-// barriers (1.1).  Half the columns in each of two CTAs an SM took 899 us
+// b4 L2048 H32 G8 P64 N128: 400 us, 543 MB from HBM (1.4 TB/s).  Bound by
+// latency between its barriers: the tiles of a head take 208 KB, so one CTA an
+// SM, whose sixteen warps issue in 41 % of the clocks and keep the matrix pipe
+// busy for 29 %; what waits is fixed latencies (2.0 clocks an instruction),
+// shared memory (1.4), barriers (1.3) and global loads of the state that leaves
+// (1.1).  Half the columns in each of two CTAs an SM took 899 us
 // against 461 at that step, since P and Z are then formed twice.
 #pragma once
 

@@ -25,7 +25,7 @@
 // FMA, the column of A broadcast from shared memory), M.  Bound by issue and
 // the latency of shared memory in the substitution (issue slots 41 % busy, six
 // CTAs an SM): b8 L2048 H80 N128, 40960 heads of chunks (368 MB
-// written), 158 us, 2.3 TB/s.
+// written), 160 us, 2.3 TB/s.
 #pragma once
 
 #include "ssd_delta.cuh"

@@ -8,8 +8,8 @@
 // values each (float4), so short rows share a warp; a lane holds kRows rows at
 // once, all loaded before any is used.
 //
-// 256 rows of H80 P64 N128 (671 MB of state): 201 us, 6.7 TB/s, a little above
-// a plain copy's rate.  CTAs of 256 threads took 251 us (the loads of a CTA
+// 256 rows of H80 P64 N128 (671 MB of state): 201 to 212 us from box to box, 6.3
+// to 6.7 TB/s, a plain copy's rate.  CTAs of 256 threads took 251 us (the loads of a CTA
 // come in one burst, and half as many CTAs overlap), four rows a lane 223 us,
 // sixteen 667 us; without the streaming hints 208 us.  The hints cost nothing
 // where the state stays in L2 (21 MB: 7.6 us with or without).

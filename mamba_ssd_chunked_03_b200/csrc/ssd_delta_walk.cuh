@@ -24,7 +24,7 @@
 // wait for one another: alone on its scheduler (128 CTAs: b4 L2048 H32 P64
 // N128, without y: 149 us) a warp issues in 29 % of the clocks and holds the
 // matrix pipe for 28 %.  Three CTAs an SM fill the gaps of one another: b8
-// L2048 H80 P64 N128 takes 525 us; the matrix instructions by themselves (228 a
+// L2048 H80 P64 N128 takes 530 us; the matrix instructions by themselves (228 a
 // warp and chunk, 8 clocks each) would take 265 us there.  A third of them are
 // y's.  With one term of S, U and M for y in bf16 (184 instructions, errors of
 // 2^-12 before y's own rounding) the walk took 460 us; it is not kept, so that y

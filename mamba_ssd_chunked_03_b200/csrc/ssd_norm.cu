@@ -4,22 +4,23 @@
 //     dw = sum_rows dout SiLU(z) n,  db = sum_rows dout SiLU(z)
 //     dz = dout (n w + b) SiLU'(z)
 //
-// Bound by HBM: every tensor is read once and every output written once.  A
+// Bound by HBM: every tensor is read once and every output written once, but for
+// rows that are swept from memory (below).  A
 // row belongs to a group of GT threads (part of a warp, or a whole CTA), which
 // holds it in registers: the mean first, then the mean square of the
 // differences to it, so that a large mean costs no accuracy.  In fp32 the
 // differences' own mean is taken out of them again: it is what the rounding of
 // the mean is off by.  In bf16 the sum of equal values is exact (8 bits each), so
 // a mean divided without error leaves zeros, and other rows deviate by more than
-// the mean's rounding shows.  Groups walk the rows
-// with a fixed stride and load the next row before they work on this one;
-// weights, biases and the sums of their gradients stay in registers all the
-// way.  The backward's partial sums (one set a CTA) are added by a second
+// the mean's rounding shows.  Groups walk the rows with a fixed stride and load
+// the next row before they work on this one; weights, biases and the sums of
+// their gradients stay in registers all the way.  The backward's partial sums (one set a CTA) are added by a second
 // kernel in a fixed order.  Rows wider than the registers hold are swept
 // several times from memory instead, with the column sums in a pass of their
-// own.  1.3 M rows of 64, gated, bf16: 87 us, 5.8 TB/s; 100003 rows of
-// 129, gated, fp32, backward: 65 us, 4.0 TB/s (bound by the instructions of its
-// four-byte loads); 7 rows of 5120: 3.7 us, a chain of latencies.
+// own.  1.3 M rows of 64, gated, bf16: 86 us, 5.8 TB/s (the call 91); 100003
+// rows of 129, gated, fp32, backward: 70 us, 3.7 TB/s (bound by the instructions
+// of its four-byte loads and of the gate); 7 rows of 5120: 3.7 us, a chain of
+// latencies.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -407,7 +408,8 @@ __device__ __forceinline__ void copy16(void* to, const void* from) {
 // two tensors at most: what takes the time is the chain of a row's sums through
 // the barrier, and two rows share one.  (16384 rows of 5120, backward: 138 us
 // with rows held in registers, 122 us from the ring one at a time, 117 us two
-// at a time: 4.3 TB/s.  Three CTAs an SM with half the ring took 133 us.)
+// at a time: 4.3 TB/s.  Three CTAs an SM with half the ring took 133 us.
+// Forward, the same rows: 100 us, with the gate 154, 0.5 of a copy's rate.)
 template <int VPL, bool BWD, bool GATE>
 struct RowRing {
   static constexpr int kTensors = 1 + GATE + BWD;
@@ -708,8 +710,10 @@ int64_t ctas(int per_sm, int threads) {
 }
 constexpr int kRowParts = 16384;  // CTAs of an SM times columns, where a row takes a CTA, are at most this
 
-// One grid of the CTAs that fit: the kernel's registers allow MINB CTAs of BT
-// threads an SM, or more of fewer.  `threads`: of a CTA that takes one row;
+// One grid of the CTAs that registers allow: MINB of BT threads an SM, or more of
+// fewer.  (The ring of a wide row can allow fewer still: two of three at 5120
+// columns forward, one with the gate, and the grid then runs in two or three
+// parts.)  `threads`: of a CTA that takes one row;
 // else GT threads take one.
 template <typename T, int E, int GT, int VPL, int BT, int MINB, bool BWD>
 cudaError_t launch(const Args& a, cudaStream_t st, int* parts, int threads = kThreads) {
@@ -760,7 +764,13 @@ cudaError_t launch_narrow(const Args& a, cudaStream_t st, int* parts, bool* wide
 
 // The group by the row's packs: part of a warp up to 64 packs (no barrier),
 // else a CTA of as many threads as the row needs with one or two packs each.
-// `vec`: elements to which every row is aligned (E, 2 or 1).
+// `vec`: elements to which every row is aligned (E, 2 or 1).  Where a row's
+// registers or its ring end, at 1024 packs, 4096 pairs or 4096 single elements, it
+// is swept from memory.  In fp32 that puts aligned rows of 4100 to 8192 columns
+// behind those that only pairs divide: 16384 rows of 5120 take 193 us forward, 442
+// gated, 397 and 922 backward, where 5122 columns take 170, 258, 328 and 956;
+// packs held beyond 1024 are not built.  bf16 rows of 10240 (8192 of them): 190,
+// 385, 416 and 786 us, 0.16 to 0.27 of a copy's rate.
 template <typename T, bool BWD>
 cudaError_t launch_rows(const Args& a, int vec, cudaStream_t st, int* parts, bool* wide) {
   constexpr int E = 16 / (int)sizeof(T), kB = BWD ? 2 : 4;

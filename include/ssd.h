@@ -586,9 +586,7 @@ SSD_API ssd_status ssd_delta_step(const ssd_delta_step_args* args, void* stream)
  *
  * The states are recomputed from the inputs; what the forward returned is not
  * read.  A gradient has its input's type, rounded once: dq, dk and dv dtype,
- * the others fp32.  dg is formed from sums of dq.q - dv.v over up to 32 tokens
- * of a head, and rounded relative to their terms; it is zero where exp(g) is.
- * Every sum is taken in a fixed order, so results are
+ * the others fp32.  Every sum is taken in a fixed order, so results are
  * deterministic.  Unlike ssd_bwd, gradients of per-sequence final states are
  * taken. */
 typedef struct {
@@ -608,8 +606,8 @@ typedef struct {
   size_t workspace_bytes;
 } ssd_delta_bwd_args;
 
-/* Workspace bytes ssd_delta_bwd needs (as above, with the presence of
- * dfinal_states and the place of dy), or 0 if the sizes are invalid. */
+/* Workspace bytes ssd_delta_bwd needs (as above, and whether dy lies on a
+ * 16-byte boundary), or 0 if the sizes are invalid. */
 SSD_API size_t ssd_delta_bwd_workspace_size(const ssd_delta_bwd_args* args);
 
 SSD_API ssd_status ssd_delta_bwd(const ssd_delta_bwd_args* args, void* stream);

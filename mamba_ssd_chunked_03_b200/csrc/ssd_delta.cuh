@@ -42,13 +42,9 @@ struct Chunk {
   int32_t tok, n;
 };
 
-// A checkpoint's place: the (up to) 64 tokens it covers, their first chunk; for
-// the last ones of a run the index of its final state, and for the first ones
-// the row whose initial state it starts from (-1: none; kInside: not the last,
-// or first, ones).
-constexpr int kInside = -2;
+// A checkpoint's place: the (up to) 64 tokens it covers, their first chunk.
 struct Slot {
-  int32_t tok, n, chunk, fin, h0;
+  int32_t tok, n, chunk;
 };
 
 // ---------------------------------------------------------------- elements

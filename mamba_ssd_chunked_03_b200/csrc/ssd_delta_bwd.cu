@@ -12,14 +12,13 @@ using namespace ssd::delta;
 namespace {
 
 struct Layout {
-  size_t runs, tokens, fwd, rev, e, d, s, ds, s_fin, max_y, max_e, max_d, max_s, max_ds, part, qdq, dvv, pi, dot, v, dy, total;
+  size_t runs, tokens, fwd, rev, e, d, s, ds, max_y, max_e, max_d, max_s, max_ds, part, dg, v, dy, total;
   int nslices, splits, heads, pg;
 };
 
 int64_t pitch_e(const Shape& s) { return (s.P + 3) / 4 * 4; }
 
 Layout layout(const Shape& s, const ssd_delta_bwd_args* b) {
-  const bool dfinal = b->dfinal_states != nullptr;
   Layout l;
   size_t at = runs_bytes(s);
   l.runs = 0;
@@ -45,14 +44,10 @@ Layout layout(const Shape& s, const ssd_delta_bwd_args* b) {
   l.d = take(tokens * s.H * pitch_e(s) * 4);
   l.s = take((size_t)s.slots * hpn * 4);
   l.ds = take((size_t)s.slots * hpn * 4);
-  l.s_fin = take(dfinal ? (size_t)s.runs * hpn * 4 : 0);
   const size_t cm = (size_t)s.chunks * s.H * l.pg * 4, sm = (size_t)s.slots * s.H * l.pg * 4;
   l.max_y = take(cm), l.max_e = take(cm), l.max_d = take(cm), l.max_s = take(sm), l.max_ds = take(sm);
   l.part = take(l.splits > 1 ? (size_t)l.splits * 2 * tokens * s.G * s.N * 4 : 0);
-  l.qdq = take((size_t)l.nslices * tokens * s.H * 4);
-  l.dvv = take(tokens * s.H * 4);
-  l.pi = take((size_t)l.nslices * s.slots * s.H * 4);
-  l.dot = take((size_t)s.b * s.H * l.pg * 4);
+  l.dg = take(l.nslices > 1 ? (size_t)l.nslices * tokens * s.H * 4 : 0);
   l.v = take(pad_bytes(s, b->fwd.v));
   l.dy = take(pad_bytes(s, b->dy));
   l.total = at;
@@ -90,23 +85,22 @@ cudaError_t run_all(const ssd_delta_bwd_args* b, const Shape& s, const Layout& l
   w.slices = (int)((s.P + kP - 1) / kP), w.units = s.runs * s.H * w.slices;
   w.tokens = p.tokens, w.heads = p.fwd, w.v = v, w.s0 = a->initial_states, w.runs = runs.runs;
   w.pg = l.pg, w.out = at(l.e), w.max_out = at(l.max_e);
-  w.check = at(l.s), w.max_check = at(l.max_s), w.fin = b->dfinal_states ? at(l.s_fin) : nullptr;
+  w.check = at(l.s), w.max_check = at(l.max_s);
   if ((e = launch_walk<T, kStates>(w, st)) != cudaSuccess) return e;
   w.heads = p.rev, w.v = dy, w.s0 = b->dfinal_states, w.out = b->dv, w.out_f = at(l.d);
   w.max_v = at(l.max_y), w.max_out = at(l.max_d), w.check = at(l.ds), w.max_check = at(l.max_ds);
-  w.fin = b->dinitial_states, w.h0 = a->initial_states, w.dot = at(l.dot);
+  w.fin = b->dinitial_states;
   w.out_vec = s.P * esz % 16 == 0 && aligned(b->dv, 16);
   if ((e = launch_rwalk<T>(w, st)) != cudaSuccess) return e;
   GradArgs g = {};
   g.L = s.L, g.H = s.H, g.G = s.G, g.P = s.P, g.N = s.N, g.hpg = p.hpg;
   g.per_row = (int)((s.L + kCheck - 1) / kCheck), g.splits = l.splits, g.heads = l.heads, g.nslices = l.nslices;
-  g.pg = l.pg, g.scale = s.scale, g.tokens = p.tokens, g.head = p.rev, g.v = v, g.dy = dy, g.g = a->g, g.pv = pv, g.pe = w.pe;
-  g.e = at(l.e), g.d = at(l.d), g.s = at(l.s), g.ds = at(l.ds), g.s_fin = b->dfinal_states ? at(l.s_fin) : nullptr;
+  g.pg = l.pg, g.scale = s.scale, g.tokens = p.tokens, g.head = p.rev, g.dy = dy, g.pv = pv, g.pe = w.pe;
+  g.e = at(l.e), g.d = at(l.d), g.s = at(l.s), g.ds = at(l.ds);
   g.max_y = at(l.max_y), g.max_e = at(l.max_e), g.max_d = at(l.max_d), g.max_s = at(l.max_s), g.max_ds = at(l.max_ds);
-  g.dot = a->initial_states ? at(l.dot) : nullptr;
   g.slots = runs.slots, g.slots_n = s.slots, g.dq = b->dq, g.dk = b->dk;
   g.part = at(l.part), g.part_size = s.b * s.L * s.G * s.N;
-  g.qdq = at(l.qdq), g.part_stride = s.b * s.L * s.H, g.dvv = at(l.dvv), g.pi = at(l.pi), g.dbeta = b->dbeta;
+  g.dg = l.nslices > 1 ? at(l.dg) : b->dg, g.dg_size = s.b * s.L * s.H, g.dbeta = b->dbeta;
   g.pair = s.N % 2 == 0 && aligned(b->dq, 2 * esz) && aligned(b->dk, 2 * esz);
   return launch_grads<T>(g, b->dg, st);
 }

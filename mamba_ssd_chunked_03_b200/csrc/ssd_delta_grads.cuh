@@ -7,18 +7,20 @@
 //   dq = P K + scale exp(cs) dY S
 //   dk = P^T Q + (Z + Z^T) K - beta exp(cs) D S + exp(cs_C - cs) beta E dS
 //   dbeta_t = d_t.e_t
-//   dg_t = sum_{s >= t} (dq_s.q_s - dv_s.v_s) + <dS, S_C>     (this head's dq; S_C the state that leaves)
+//   dg_t = sum_{s < t <= r} W_rs + sum_{r >= t} A_r + sum_{s < t} B_s + exp(cs_C) <dS, S>   (for each head)
+//     W_rs = P_rs q_r.k_s + Z_rs k_r.k_s,  B_s = exp(cs_C - cs_s) beta_s e_s.(dS k_s)
+//     A_r = scale exp(cs_r) dy_r.(S q_r) - beta_r exp(cs_r) d_r.(S k_r)
 //
-// dg by the last line takes each token's pi_t = <G_t, S_t> from the next one's
-// (pi_{t-1} = dg_t + dy_{t-1}.y_{t-1}, dg_t = pi_t - dv_t.v_t, and dy.y = dq.q).
-// <dS, S> is known at both ends of the 64 tokens (dg_0 is that of the tokens
-// before; at a row's start <dS, S> of the initial state, from the reverse walk), so
-// the sums run from the nearer end, over 32 tokens at most, and rounding does not
-// pile up along the sequence.  It is relative to those sums' terms; where exp(g) is
-// zero, dg is zero and the sums start anew.  All operands that are results
-// are split in two terms: dg needs dq to fp32 accuracy, and what is returned is
-// rounded once.  (One term for dk's in bf16, errors of 2^-12 before its own
-// rounding: 354 us where it now takes 400.)
+// dg_t is the sum of all that passes token t, each term with its decay in it, so it
+// is held to its own size however small that is.  (dg_t = dg_{t+1} + dq_t.q_t -
+// dv_t.v_t costs less, but leaves the rounding of terms that do not pass t: at
+// exp(g) = 1e-6 a thousandth of dg, and noise where it is zero.)  A and B are the
+// products of what the state's products add to dq and dk with q and k; the sums of
+// W are taken in the registers that hold P and Z, 16 x 16 tokens a warp, and put
+// together by one thread a token.  All operands that are results are split in two
+// terms, and what is returned is rounded once.  (One term for dk's in bf16, errors
+// of 2^-12 before its own rounding: 354 us where it now takes 424, of which dg as it
+// is now some 20.)
 //
 // One CTA takes 64 tokens of a group, a slice of the columns n, and some of the
 // group's heads, whose dq and dk it adds in registers in a fixed order; sixteen
@@ -26,12 +28,11 @@
 // twice the columns each took 1.24 times as long: between its barriers a warp's
 // instructions depend on one another, and two warps a scheduler do not fill it.)
 //
-// b4 L2048 H32 G8 P64 N128: 400 us, 543 MB from HBM (1.4 TB/s).  Bound by
-// latency between its barriers: the tiles of a head take 208 KB, so one CTA an
-// SM, whose sixteen warps issue in 41 % of the clocks and keep the matrix pipe
-// busy for 29 %; what waits is fixed latencies (2.0 clocks an instruction),
-// shared memory (1.4), barriers (1.3) and global loads of the state that leaves
-// (1.1).  Half the columns in each of two CTAs an SM took 899 us
+// b4 L2048 H32 G8 P64 N128: 424 us, 507 MB from HBM (1.2 TB/s).  Bound by latency
+// between its barriers: the tiles of a head take 220 KB, so one CTA an SM, whose
+// sixteen warps issue in 40 % of the clocks and keep the matrix pipe busy for 28 %;
+// what waits is barriers (2.2 clocks an instruction: the sums of W are some of the
+// warps' only), fixed latencies (1.9) and shared memory (1.3).  Half the columns in each of two CTAs an SM took 899 us
 // against 461 at that step, since P and Z are then formed twice.
 #pragma once
 
@@ -53,28 +54,22 @@ struct GradArgs {
   float scale;
   const char* tokens;  // TokenTiles of both 32-token chunks
   const char* head;    // RevTiles: factors and decays
-  const void* v;
   const void* dy;
-  const float* g;
   const float* e;
   const float* d;
   const float* s;       // [slot][head][P][N] states that enter
   const float* ds;      // gradients of the states that leave
-  const float* s_fin;   // [run][head][P][N] last states, or null (no gradient comes in there)
   const float *max_y, *max_e, *max_d, *max_s, *max_ds;
   const Slot* slots;    // packed, or null
   void* dq;
   void* dk;
   float* part;          // [split][2][tokens][G][N], with several splits
   int64_t part_size;    // tokens G N
-  float* qdq;           // [nslice][tokens][H]
-  int64_t part_stride;  // tokens H
-  float* dvv;           // [tokens][H]
-  float* pi;            // [nslice][slot][H]
+  float* dg;            // [nslice][tokens][H]: with one slice, the gradient itself
+  int64_t dg_size;      // tokens H
   float* dbeta;
   int64_t slots_n;
-  int64_t pv, pe;       // row pitches of v and dy, and of e and d: multiples of four
-  const float* dot;     // [row][head][pg] <gradient, initial state>, or null: there is none
+  int64_t pv, pe;       // row pitches of dy, and of e and d: multiples of four
   int pair;             // dq and dk can be written by twos
 };
 
@@ -97,9 +92,12 @@ struct GradTiles {
   static constexpr int kZb = kZa + 2 * kSmall;         // Z with k's scales by column
   static constexpr int kEnd = kZb + 2 * kSmall;
   static_assert(kY + kTerms * kSmall <= kEnd, "the operands of a piece");
-  // E, D, V and dY of the next piece as they are in memory
-  static constexpr int kRawE = kEnd, kRawD = kRawE + 64 * 64 * 4;
-  static constexpr int kRawV = kRawD + 64 * 64 * 4, kRawY = kRawV + 64 * 64 * (int)sizeof(T);
+  // q k^T and k k^T of the group's tokens: eight values each of every thread of
+  // the ten warps whose block lies on or below the diagonal
+  static constexpr int kGram = kEnd;
+  // E, D and dY of the next piece as they are in memory
+  static constexpr int kRawE = kGram + 10 * 32 * 64, kRawD = kRawE + 64 * 64 * 4;
+  static constexpr int kRawY = kRawD + 64 * 64 * 4;
   static constexpr int kRawEnd = kRawY + 64 * 64 * (int)sizeof(T);
   // fp32 pieces are read when they are needed
   static constexpr bool kAhead = sizeof(T) == 2;
@@ -158,6 +156,34 @@ __device__ __forceinline__ void add_rows(float (&to)[TN][4], const float (&x)[TN
     to[i][2] = fmaf(x[i][2], f1, to[i][2]), to[i][3] = fmaf(x[i][3], f1, to[i][3]);
   }
 }
+// The same with a second factor for all, where the product of both may be too
+// small for a number.
+template <int TN>
+__device__ __forceinline__ void add_rows(float (&to)[TN][4], const float (&x)[TN][4], float f0, float f1, float f) {
+#pragma unroll
+  for (int i = 0; i < TN; ++i) {
+    to[i][0] = fmaf(x[i][0] * f0, f, to[i][0]), to[i][1] = fmaf(x[i][1] * f0, f, to[i][1]);
+    to[i][2] = fmaf(x[i][2] * f1, f, to[i][2]), to[i][3] = fmaf(x[i][3] * f1, f, to[i][3]);
+  }
+}
+// the rows' products with those of a tile of tokens (columns n0.., TERMS terms, unscaled)
+template <int TN, int W, int TERMS>
+__device__ __forceinline__ float2 dot_rows(const float (&x)[TN][4], const char* tile, int term_bytes, int r0, int n0, int lane) {
+  float d[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const uint32_t o = tile_off<W>(r0 + 8 * hh, n0 + 8 * i + 2 * (lane & 3));
+      float2 q = unpack2(*reinterpret_cast<const uint32_t*>(tile + o));
+      if constexpr (TERMS == 2) {
+        const float2 l = unpack2(*reinterpret_cast<const uint32_t*>(tile + term_bytes + o));
+        q.x += l.x, q.y += l.y;
+      }
+      d[hh] = fmaf(q.x, x[i][2 * hh], fmaf(q.y, x[i][2 * hh + 1], d[hh]));
+    }
+  return make_float2(d[0], d[1]);
+}
 
 // four scaled values as fp16 terms at byte offset o of a tile
 template <int TERMS>
@@ -193,7 +219,6 @@ __device__ __forceinline__ Slot row_slot(const GradArgs& a, int64_t slot) {
   Slot s;
   s.tok = (int)(row * a.L + i * kCheck), s.n = a.L - i * kCheck < kCheck ? (int)(a.L - i * kCheck) : kCheck;
   s.chunk = (int)(row * ((a.L + kC - 1) / kC) + 2 * i);
-  s.fin = i + 1 < a.per_row ? kInside : (int)row, s.h0 = i > 0 ? kInside : (int)row;
   return s;
 }
 
@@ -236,7 +261,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
   __shared__ float whole[2];  // of the chunks that exist
   __shared__ int plain[2];
   __shared__ float scale[5], iscale[5];       // of Y, E, D, S, dS
-  __shared__ float sums[6][kCheck];           // d.e, dv.v, and q.dq of each quarter of the columns
+  __shared__ float dde[kCheck];               // d.e
+  __shared__ float past[4][kCheck], next[4][kCheck];  // A and B of each quarter of the columns
+  __shared__ float rows_w[10][16], cols_w[10][16];    // of the blocks of W: sums over the columns before a token of
+                                                      // the rows from it on; over all rows of the columns before it
   __shared__ float wmax[3][kGradWarps], wpi[kGradWarps];
   const uint32_t smu = sm100::smem_u32(sm);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mt = warp & 3, quarter = warp >> 2;
@@ -270,15 +298,53 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
     ik[t] = t < kC * nch ? decays(t >> 5, h0)->ik[t & 31] : 1.f;
     iq[t] = t < kC * nch ? decays(t >> 5, h0)->iq[t & 31] : 1.f;
   }
+  __syncthreads();
+  const int sb = quarter;  // this warp's block of P, Z and W: columns 16 sb.., if not above the diagonal
+  const int r0 = 16 * mt + (lane >> 2);  // this thread's rows: r0, r0 + 8
+  const int blk = mt * (mt + 1) / 2 + sb;
+  if (sb <= mt) {  // q k^T and k k^T
+    float x[2][4], z[2][4];
+    clear(x);
+    clear(z);
+    const int br = (lane & 7) + (lane >> 4) * 8, bc = ((lane >> 3) & 1) * 8;
+#pragma unroll 2
+    for (int k = 0; k < NS / 16; ++k) {
+      uint32_t Q[TM][4], K[TM][4], B[TM][4];
+#pragma unroll
+      for (int t = 0; t < TM; ++t) {
+        a_frag<NS, false>(smu + G::kQ + t * G::kTok, 16 * mt, 16 * k, lane, Q[t]);
+        a_frag<NS, false>(smu + G::kK + t * G::kTok, 16 * mt, 16 * k, lane, K[t]);
+        ldsm4(smu + G::kK + t * G::kTok + tile_off<NS>(16 * sb + br, 16 * k + bc), B[t]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mma(x[i], Q[0], B[0][2 * i], B[0][2 * i + 1]);
+        mma(z[i], K[0], B[0][2 * i], B[0][2 * i + 1]);
+        if constexpr (TM == 2) {
+          mma(x[i], Q[0], B[TM - 1][2 * i], B[TM - 1][2 * i + 1]);
+          mma(z[i], K[0], B[TM - 1][2 * i], B[TM - 1][2 * i + 1]);
+          mma(x[i], Q[TM - 1], B[0][2 * i], B[0][2 * i + 1]);
+          mma(z[i], K[TM - 1], B[0][2 * i], B[0][2 * i + 1]);
+        }
+      }
+    }
+    float4* const to = reinterpret_cast<float4*>(sm + G::kGram) + blk * 128 + lane;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 ks = *reinterpret_cast<const float2*>(ik + 16 * sb + 8 * i + 2 * (lane & 3));
+      to[64 * i] = make_float4(x[i][0] * iq[r0] * ks.x, x[i][1] * iq[r0] * ks.y, x[i][2] * iq[r0 + 8] * ks.x,
+                               x[i][3] * iq[r0 + 8] * ks.y);
+      to[64 * i + 32] = make_float4(z[i][0] * ik[r0] * ks.x, z[i][1] * ik[r0] * ks.y, z[i][2] * ik[r0 + 8] * ks.x,
+                                    z[i][3] * ik[r0 + 8] * ks.y);
+    }
+  }
   float dq[TN][4], dk[TN][4];
   clear(dq);
   clear(dk);
-  const int r0 = 16 * mt + (lane >> 2);  // this thread's rows: r0, r0 + 8
-  const int sb = quarter;                // this warp's block of P and Z: columns 16 sb.., if not above the diagonal
 
   // A piece is 64 columns of headdim of one head.  What the next piece needs is
-  // copied while this one is worked on: decays and largest magnitudes, E, D, V
-  // and dY, and, where this piece's operands have been used up, the states.
+  // copied while this one is worked on: decays and largest magnitudes, E, D and
+  // dY, and, where this piece's operands have been used up, the states.
   const bool n4 = a.N % 4 == 0;
   const auto copy_small = [&](int64_t h, int p0) {
     if (h >= h1) return;
@@ -314,7 +380,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
         const int64_t th = ((int64_t)sl.tok + t) * a.H + h, oe = th * a.pe + p0 + p, ov = th * a.pv + p0 + p;
         copy4(sm + G::kRawE + (t * 64 + p) * 4, a.e, oe, left, true);
         copy4(sm + G::kRawD + (t * 64 + p) * 4, a.d, oe, left, true);
-        copy4(sm + G::kRawV + (t * 64 + p) * (int)sizeof(T), static_cast<const T*>(a.v), ov, left, true);
         copy4(sm + G::kRawY + (t * 64 + p) * (int)sizeof(T), static_cast<const T*>(a.dy), ov, left, true);
       }
     }
@@ -339,18 +404,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
       }
     }
   };
-  const float* sc = sl.fin == kInside ? a.s + (slot + 1) * a.H * a.P * a.N
-                    : a.s_fin && sl.fin >= 0 ? a.s_fin + (int64_t)sl.fin * a.H * a.P * a.N : nullptr;
   copy_small(h0, 0);
   copy_rows(h0, 0);
   copy_states(h0, 0);
   cp_async_commit();
   for (int64_t h = h0; h < h1; ++h) {
-    float P[2][4], Z[2][4], dqh[TN][4];
+    float P[2][4], Z[2][4];
     clear(P);
     clear(Z);
-    clear(dqh);
     float pi = 0.f;
+    float2 ra = make_float2(0.f, 0.f), rb = ra;  // A and B of this thread's rows
     for (int p0 = 0; p0 < a.P; p0 += kPS) {
       const int64_t hn = p0 + kPS < a.P ? h : h + 1;  // the next piece
       const int pn = p0 + kPS < a.P ? p0 + kPS : 0;
@@ -362,7 +425,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
           if (t >= kC * nch) intol[t] = outl[t] = inv[t] = 1.f, bet[t] = 0.f;
           into[t] = intol[t] * (t >= kC && nch == 2 ? whole[0] : 1.f);
           outof[t] = outl[t] * (t < kC && nch == 2 ? whole[1] : 1.f);
-          sums[0][t] = sums[1][t] = 0.f;
+          dde[t] = 0.f;
         }
       } else if (threadIdx.x < kCheck + 5) {
         const int w = threadIdx.x - kCheck;
@@ -371,20 +434,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
         for (int i = 0; i < 8; ++i) m = fmaxf(m, most[w][i]);
         scale[w] = pow2_scale(m, iscale[w]);
       }
-      {  // the states to operands, and <dS, S_C>
-        float xs[kSt][4], xd[kSt][4], xc[kSt][4];
+      {  // the states to operands, and <dS, S>
+        float xs[kSt][4], xd[kSt][4];
 #pragma unroll
         for (int i = 0; i < kSt; ++i) {
           int p, n;
           const int left = state_at(i, p0, p, n);
-          const int64_t o = (h * a.P + p0 + p) * a.N + n0 + n;
-          get4(sc ? sc + o : a.s, sc ? left : 0, n4, xc[i]);
           if constexpr (G::kAhead) {
             get4(reinterpret_cast<const float*>(sm + G::kS) + (threadIdx.x + i * kGradThreads) * 4, xs[i]);
             get4(reinterpret_cast<const float*>(sm + G::kDS) + (threadIdx.x + i * kGradThreads) * 4, xd[i]);
           } else {
-            get4(a.s + slot * a.H * a.P * a.N + o, left, n4, xs[i]);
-            get4(a.ds + slot * a.H * a.P * a.N + o, left, n4, xd[i]);
+            const int64_t o = ((slot * a.H + h) * a.P + p0 + p) * a.N + n0 + n;
+            get4(a.s + o, left, n4, xs[i]);
+            get4(a.ds + o, left, n4, xd[i]);
           }
         }
         __syncthreads();  // the copied tiles are read; factors and scales are there
@@ -396,35 +458,30 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
           put4<2>(sm + G::kS, G::kTok, to, xs[i], scale[3]);
           put4<2>(sm + G::kDS, G::kTok, to, xd[i], scale[4]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) pi = fmaf(xd[i][e], xc[i][e], pi);
+          for (int e = 0; e < 4; ++e) pi = fmaf(xd[i][e], xs[i][e], pi);
         }
       }
 #pragma unroll
-      for (int x = 0; x < 64 * 16 / kGradThreads; ++x) {  // E, D and dY to operands; d.e and d.v
+      for (int x = 0; x < 64 * 16 / kGradThreads; ++x) {  // E, D and dY to operands; d.e
         const int t = (threadIdx.x >> 4) + (kGradThreads / 16) * x, p = (threadIdx.x & 15) * 4;
-        float e4[4], d4[4], u4[4], y4[4];
+        float e4[4], d4[4], y4[4];
         if constexpr (G::kAhead) {
           get4(reinterpret_cast<const float*>(sm + G::kRawE) + t * 64 + p, e4);
           get4(reinterpret_cast<const float*>(sm + G::kRawD) + t * 64 + p, d4);
           get4(reinterpret_cast<const T*>(sm + G::kRawY) + t * 64 + p, y4);
-          get4(reinterpret_cast<const T*>(sm + G::kRawV) + t * 64 + p, u4);
         } else {
           const int left = t < sl.n ? (int)(a.P - p0 - p) : 0;
           const int64_t th = ((int64_t)sl.tok + t) * a.H + h, oe = th * a.pe + p0 + p, ov = th * a.pv + p0 + p;
           get4(a.e + oe, left, true, e4);
           get4(a.d + oe, left, true, d4);
           get4(static_cast<const T*>(a.dy) + ov, left, true, y4);
-          get4(static_cast<const T*>(a.v) + ov, left, true, u4);
         }
-        float de = 0.f, dv = 0.f;
+        float de = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) de = fmaf(d4[i], e4[i], de), dv = fmaf(d4[i], u4[i], dv);
+        for (int i = 0; i < 4; ++i) de = fmaf(d4[i], e4[i], de);
 #pragma unroll
-        for (int i = 8; i > 0; i >>= 1) {
-          de += __shfl_xor_sync(0xffffffffu, de, i);
-          dv += __shfl_xor_sync(0xffffffffu, dv, i);
-        }
-        if ((lane & 15) == 0) sums[0][t] += de, sums[1][t] += dv;  // one thread of its own for each t
+        for (int i = 8; i > 0; i >>= 1) de += __shfl_xor_sync(0xffffffffu, de, i);
+        if ((lane & 15) == 0) dde[t] += de;  // one thread of its own for each t
         const uint32_t to = tile_off<64>(t, p);
         put4<2>(sm + G::kE, G::kSmall, to, e4, scale[1]);
         put4<2>(sm + G::kD, G::kSmall, to, d4, scale[2]);
@@ -458,21 +515,27 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
             mma(z[i], D[1], E[0][2 * i], E[0][2 * i + 1]);
           }
         }
-        add_rows(P, x, iy * ie, iy * ie);
-        add_rows(Z, z, id * ie, id * ie);
+        add_rows(P, x, iy, iy, ie);
+        add_rows(Z, z, id, id, ie);
       }
       float tmp[TN][4];
       const int nb = quarter * (NS / 4);
       const float in0 = into[r0], in1 = into[r0 + 8], be0 = bet[r0], be1 = bet[r0 + 8];
       clear(tmp);
       product<TN, 64, false, TM, NS, 2>(tmp, smu + G::kY, G::kSmall, 16 * mt, smu + G::kS, G::kTok, nb, 0, kPS / 16, lane);
-      add_rows(dqh, tmp, a.scale * in0 * (iy * is), a.scale * in1 * (iy * is));
+      // a row's product with its q or k is what it gives to A or B, as it is added
+      const auto add = [&](float (&to)[TN][4], float f0, float f1, float f, float2& sum, int tile, const float* inv_scale) {
+        const float2 d = dot_rows<TN, NS, TM>(tmp, sm + tile, G::kTok, r0, nb, lane);
+        sum.x = fmaf(d.x * inv_scale[r0] * f0, f, sum.x), sum.y = fmaf(d.y * inv_scale[r0 + 8] * f1, f, sum.y);
+        add_rows(to, tmp, f0, f1, f);
+      };
+      add(dq, a.scale * in0 * iy, a.scale * in1 * iy, is, ra, G::kQ, iq);
       clear(tmp);
       product<TN, 64, false, 2, NS, 2>(tmp, smu + G::kD, G::kSmall, 16 * mt, smu + G::kS, G::kTok, nb, 0, kPS / 16, lane);
-      add_rows(dk, tmp, -be0 * in0 * (id * is), -be1 * in1 * (id * is));
+      add(dk, -be0 * in0 * id, -be1 * in1 * id, is, ra, G::kK, ik);
       clear(tmp);
       product<TN, 64, false, 2, NS, 2>(tmp, smu + G::kE, G::kSmall, 16 * mt, smu + G::kDS, G::kTok, nb, 0, kPS / 16, lane);
-      add_rows(dk, tmp, be0 * outof[r0] * (ie * ids), be1 * outof[r0 + 8] * (ie * ids));
+      add(dk, be0 * outof[r0] * ie, be1 * outof[r0 + 8] * ie, ids, rb, G::kK, ik);
       if (hn == h) {  // another piece of this head
         __syncthreads();
         copy_small(hn, pn);
@@ -508,6 +571,63 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
             m3 = fmaxf(m3, fmaxf(fabsf(z * ik[t]), fabsf(z * ik[s])));
           }
       }
+    }
+    if (sb <= mt) {  // W, and the sums of it that dg takes
+      const float4* const from = reinterpret_cast<const float4*>(sm + G::kGram) + blk * 128 + lane;
+      float w[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 x = from[64 * i], z = from[64 * i + 32];
+        const float qk[4] = {x.x, x.y, x.z, x.w}, kk[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = r0 + 8 * (e >> 1), s = 16 * sb + 8 * i + 2 * (lane & 3) + (e & 1);
+          w[i][e] = s < t ? fmaf(P[i][e], qk[e], Z[i][e] * kk[e]) : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // over the rows from each one on
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            const float u = __shfl_down_sync(0xffffffffu, w[i][e], o), v = __shfl_down_sync(0xffffffffu, w[i][2 + e], o);
+            if (lane + o < 32) w[i][e] += u, w[i][2 + e] += v;
+          }
+          w[i][e] += __shfl_sync(0xffffffffu, w[i][2 + e], lane & 3);
+        }
+      }
+      float before = 0.f;  // all rows: the columns before each one
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float up = w[i][0] + w[i][1];
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          const float u = __shfl_up_sync(0xffffffffu, up, o);
+          if ((lane & 3) >= o) up += u;
+        }
+        const float u = __shfl_up_sync(0xffffffffu, up, 1), x = before + ((lane & 3) ? u : 0.f);
+        if (lane < 4) cols_w[blk][8 * i + 2 * lane] = x, cols_w[blk][8 * i + 2 * lane + 1] = x + w[i][0];
+        before += __shfl_sync(0xffffffffu, up, 3);
+      }
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (16 * sb + 8 * i + 2 * (lane & 3) + e < r0 + 8 * hh) x += w[i][2 * hh + e];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        if ((lane & 3) == 0) rows_w[blk][(lane >> 2) + 8 * hh] = x;
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      ra.x += __shfl_xor_sync(0xffffffffu, ra.x, o), ra.y += __shfl_xor_sync(0xffffffffu, ra.y, o);
+      rb.x += __shfl_xor_sync(0xffffffffu, rb.x, o), rb.y += __shfl_xor_sync(0xffffffffu, rb.y, o);
+    }
+    if ((lane & 3) == 0) {
+      past[quarter][r0] = ra.x, past[quarter][r0 + 8] = ra.y;
+      next[quarter][r0] = rb.x, next[quarter][r0 + 8] = rb.y;
     }
     {
       m1 = absmax_bits(__float_as_uint(m1)), m2 = absmax_bits(__float_as_uint(m2)), m3 = absmax_bits(__float_as_uint(m3));
@@ -551,7 +671,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
       const int nb = quarter * (NS / 4);
       clear(tmp);
       product<TN, 64, false, 2, NS, TM>(tmp, smu + G::kW1, G::kSmall, 16 * mt, smu + G::kK, G::kTok, nb, 0, mt + 1, lane);
-      add_rows(dqh, tmp, i1, i1);
+      add_rows(dq, tmp, i1, i1);
       clear(tmp);
       product<TN, 64, true, 2, NS, TM>(tmp, smu + G::kW2, G::kSmall, 16 * mt, smu + G::kQ, G::kTok, nb, mt, 4, lane);
       add_rows(dk, tmp, i2, i2);
@@ -559,43 +679,37 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
       product<TN, 64, true, 2, NS, TM>(tmp, smu + G::kZa, G::kSmall, 16 * mt, smu + G::kK, G::kTok, nb, mt, 4, lane);
       product<TN, 64, false, 2, NS, TM>(tmp, smu + G::kZb, G::kSmall, 16 * mt, smu + G::kK, G::kTok, nb, 0, mt + 1, lane);
       add_rows(dk, tmp, i3, i3);
-      // q.dq of this head
-      float q0 = 0.f, q1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const uint32_t o = tile_off<NS>(r0 + 8 * hh, nb + 8 * i + 2 * (lane & 3));
-          float2 q = unpack2(*reinterpret_cast<const uint32_t*>(sm + G::kQ + o));
-          if constexpr (TM == 2) {
-            const float2 l = unpack2(*reinterpret_cast<const uint32_t*>(sm + G::kQ + G::kTok + o));
-            q.x += l.x, q.y += l.y;
-          }
-          float& to = hh ? q1 : q0;
-          to = fmaf(q.x, dqh[i][2 * hh], fmaf(q.y, dqh[i][2 * hh + 1], to));
-        }
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        q0 += __shfl_xor_sync(0xffffffffu, q0, o);
-        q1 += __shfl_xor_sync(0xffffffffu, q1, o);
-      }
-      if ((lane & 3) == 0) sums[2 + quarter][r0] = q0 * iq[r0], sums[2 + quarter][r0 + 8] = q1 * iq[r0 + 8];
-      add_rows(dq, dqh, 1.f, 1.f);
     }
     __syncthreads();
-    if (threadIdx.x < sl.n) {
-      const int t = threadIdx.x;
-      const int64_t o = ((int64_t)sl.tok + t) * a.H + h;
-      a.qdq[(int64_t)ns * a.part_stride + o] = (sums[2][t] + sums[3][t]) + (sums[4][t] + sums[5][t]);
-      if (ns == 0) {
-        a.dbeta[o] = sums[0][t];
-        a.dvv[o] = sums[1][t] * bet[t];
-      }
-    } else if (threadIdx.x == kCheck) {
-      float s = 0.f;
+    if (threadIdx.x < kCheck) {  // dg and dbeta: two warps of 32 tokens each
+      const int t = threadIdx.x, o = t ^ 32;
+      const auto four = [](const float (&x)[4][kCheck], int i) { return (x[0][i] + x[1][i]) + (x[2][i] + x[3][i]); };
+      float from = four(past, t), upto = four(next, t), other = warp ? four(next, o) : four(past, o), all = 0.f;
 #pragma unroll
-      for (int i = 0; i < kGradWarps; ++i) s += wpi[i];
-      a.pi[((int64_t)ns * a.slots_n + slot) * a.H + h] = s;
+      for (int i = 1; i < 32; i <<= 1) {
+        const float u = __shfl_down_sync(0xffffffffu, from, i), v = __shfl_up_sync(0xffffffffu, upto, i);
+        if (lane + i < 32) from += u;
+        if (lane >= i) upto += v;
+        other += __shfl_xor_sync(0xffffffffu, other, i);
+      }
+      upto = __shfl_up_sync(0xffffffffu, upto, 1);
+      if (lane == 0) upto = 0.f;
+      if (warp) upto += other;
+      else from += other;
+#pragma unroll
+      for (int i = 0; i < kGradWarps; ++i) all += wpi[i];
+      const int m = t >> 4, r = t & 15;
+      float w = 0.f;
+      for (int i = 0; i <= m; ++i) w += rows_w[m * (m + 1) / 2 + i][r];
+      for (int n = m + 1; n < 4; ++n) {
+        for (int i = 0; i < m; ++i) w += rows_w[n * (n + 1) / 2 + i][0];
+        w += cols_w[n * (n + 1) / 2 + m][r];
+      }
+      if (t < sl.n) {
+        const int64_t at = ((int64_t)sl.tok + t) * a.H + h;
+        a.dg[(int64_t)ns * a.dg_size + at] = (all * (nch == 2 ? whole[0] * whole[1] : whole[0]) + from) + (upto + w);
+        if (ns == 0) a.dbeta[at] = dde[t];
+      }
     }
     if (h + 1 < h1) {
       __syncthreads();  // the factors are used up
@@ -635,66 +749,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) k_delta_grads(const GradArgs 
       }
 }
 
-// dg: a warp takes the 64 tokens of a slot and head, two a lane, each summed from
-// the nearer known end.  Known are <dS, S> at either end of the slot, and zero at a
-// token whose decay is zero: nothing passes it in either direction, so
-// sums neither cross it nor carry their rounding to the other side.
-__global__ void __launch_bounds__(256) k_delta_dg(const GradArgs a, float* __restrict__ dg) {
-  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= a.slots_n * a.H) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t slot = i / a.H, h = i % a.H;
-  const Slot s = a.slots ? a.slots[slot] : row_slot(a, slot);
-  if (s.n == 0) return;
-  float x[2], before = 0.f, after = 0.f;  // tokens 2 lane, 2 lane + 1: dq.q - dv.v
-  bool z[2];                              // exp(g) is zero
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int t = 2 * lane + e;
-    const int64_t o = ((int64_t)s.tok + t) * a.H + h;
-    x[e] = t < s.n ? -a.dvv[o] : 0.f;
-    z[e] = t < s.n && expf(a.g[o]) == 0.f;
-    if (t < s.n)
-      for (int c = 0; c < a.nslices; ++c) x[e] += a.qdq[c * a.part_stride + o];
-  }
-  for (int c = 0; c < a.nslices; ++c) {
-    after += a.pi[(c * a.slots_n + slot) * a.H + h];
-    if (s.h0 == kInside) before += a.pi[(c * a.slots_n + slot - 1) * a.H + h];
-  }
-  if (a.dot && s.h0 >= 0) {  // 16 rows of headdim a part: in a fixed order
-    for (int c = lane; c < a.pg; c += 32) before += a.dot[((int64_t)s.h0 * a.H + h) * a.pg + c];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  const uint32_t m0 = __ballot_sync(0xffffffffu, z[0]), m1 = __ballot_sync(0xffffffffu, z[1]);
-  const bool zn = lane < 31 && ((m0 >> (lane + 1)) & 1);  // the token after this lane's two
-  // sums over the tokens before a lane's first since the last zero, and from it to the next one
-  float up = (z[1] ? 0.f : x[0]) + x[1], down = x[0] + (z[1] ? 0.f : x[1]);
-  bool cut_up = z[0] || z[1], cut_down = z[1] || zn;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float u = __shfl_up_sync(0xffffffffu, up, o), d = __shfl_down_sync(0xffffffffu, down, o);
-    const int cu = __shfl_up_sync(0xffffffffu, (int)cut_up, o), cd = __shfl_down_sync(0xffffffffu, (int)cut_down, o);
-    if (lane >= o) up += cut_up ? 0.f : u, cut_up = cut_up || cu;
-    if (lane + o < 32) down += cut_down ? 0.f : d, cut_down = cut_down || cd;
-  }
-  const float upto = __shfl_up_sync(0xffffffffu, up, 1), rest = __shfl_down_sync(0xffffffffu, down, 1);
-  const uint32_t below = (1u << lane) - 1u;
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int t = 2 * lane + e;
-    if (t >= s.n) continue;
-    // the last zero at or before t, the next one after it (-1, 64: none)
-    const uint32_t p0 = m0 & (below | 1u << lane), p1 = e ? m1 & (below | 1u << lane) : m1 & below;
-    const uint32_t q0 = m0 & ~(below | 1u << lane), q1 = e ? m1 & ~(below | 1u << lane) : m1 & ~below;
-    const int last = max(p0 ? 2 * (31 - __clz(p0)) : -1, p1 ? 2 * (31 - __clz(p1)) + 1 : -1);
-    const int next = min(q0 ? 2 * (__ffs(q0) - 1) : 64, q1 ? 2 * (__ffs(q1) - 1) + 1 : 64);
-    const float pre = (lane && !z[0] ? upto : 0.f), suf = e ? x[1] + (zn || lane == 31 ? 0.f : rest) : down;
-    const float b = (last < 0 ? before : 0.f) - (e ? (z[1] ? 0.f : pre + x[0]) : pre);
-    const float f = (next == 64 ? after : 0.f) + suf;
-    const int away = last >= 0 ? t - last : t, to = (next < 64 ? next : s.n) - t;
-    dg[((int64_t)s.tok + t) * a.H + h] = last == t ? 0.f : away <= to ? b : f;
-  }
+// dg from the parts of the slices of the columns n, in order.
+__global__ void __launch_bounds__(256) k_delta_dg(const float* __restrict__ part, int slices, int64_t n, float* dg) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float x = 0.f;
+  for (int s = 0; s < slices; ++s) x += part[s * n + i];
+  dg[i] = x;
 }
 
 // dq and dk from the splits' parts, in order.
@@ -727,8 +788,10 @@ cudaError_t launch_grads(const GradArgs& a, float* dg, cudaStream_t stream) {
                   : a.N <= 128 ? launch_grads_nt<T, 128>(a, stream)
                                : launch_grads_nt<T, 256>(a, stream);
   if (e != cudaSuccess) return e;
-  k_delta_dg<<<(unsigned)((a.slots_n * a.H + 7) / 8), 256, 0, stream>>>(a, dg);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.nslices > 1) {
+    k_delta_dg<<<(unsigned)((a.dg_size + 255) / 256), 256, 0, stream>>>(a.dg, a.nslices, a.dg_size, dg);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   if (a.splits > 1) {
     k_delta_sum<T><<<(unsigned)((a.part_size + 255) / 256), 256, 0, stream>>>(a.part, a.splits, a.part_size,
                                                                              static_cast<T*>(a.dq), static_cast<T*>(a.dk));

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restri
     runs[i] = r;
   }
   for (int64_t i = threadIdx.x; i < places; i += kThreads) chunks[i] = Chunk{0, 0};
-  for (int64_t i = threadIdx.x; i < checks; i += kThreads) slots[i] = Slot{0, 0, 0, kInside, kInside};
+  for (int64_t i = threadIdx.x; i < checks; i += kThreads) slots[i] = Slot{0, 0, 0};
   __syncthreads();
   if (warp == 0) {
     const int c = warp_count[lane];
@@ -128,12 +128,9 @@ __global__ void __launch_bounds__(kThreads) k_delta_runs(const int32_t* __restri
     const int t = first[k], len = ranked ? lens[k] : len_of(k);
     for (int i = lane * kC; i < len; i += 32 * kC)
       chunks[t / kC + k + i / kC] = Chunk{t + i, len - i < kC ? len - i : kC};
-    const int id = seq[t];
     for (int i = lane * kCheck; i < len; i += 32 * kCheck)
       slots[t / kCheck + k + i / kCheck] =
-          Slot{t + i, len - i < kCheck ? len - i : kCheck, (int)(t / kC + k + i / kC),
-               i + kCheck < len ? kInside : id >= 0 && id < cap ? id : -1,
-               i > 0 ? kInside : t % L == 0 ? (int)(t / L) : -1};
+          Slot{t + i, len - i < kCheck ? len - i : kCheck, (int)(t / kC + k + i / kC)};
   }
   __syncthreads();
   for (int64_t i = threadIdx.x; i < cap; i += kThreads) {

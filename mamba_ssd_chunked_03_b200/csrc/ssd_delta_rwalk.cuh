@@ -116,20 +116,6 @@ __global__ void __launch_bounds__(kThreads, NT <= 128 ? 3 : 2) k_delta_rwalk(con
     as_operand<true>(d, hi, lo);
     state_add<NT, kTerms>(S, hi, lo, kt, lane);
   }
-  if (a.h0 && run.h0 >= 0 && rows > 0) {  // <gradient, initial state>, which dg starts from
-    const float* base = a.h0 + (((int64_t)run.h0 * a.H + h) * a.P + p0) * a.N;
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < NT / 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int p = (lane >> 2) + 8 * (e >> 1), n = 8 * i + 2 * (lane & 3) + (e & 1);
-        if (p < rows && n < a.N) x = fmaf(S[i][e] * (e < 2 ? unit.sig.x : unit.sig.y), base[p * a.N + n], x);
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (lane == 0) a.dot[((int64_t)run.h0 * a.H + h) * a.pg + p0 / 16] = x;
-  }
   if (a.fin && run.h0 >= 0)
     store_state<NT>(S, unit.sig.x, unit.sig.y, a.fin + (((int64_t)run.h0 * a.H + h) * a.P + p0) * a.N, a.N, rows, lane);
 }

@@ -66,8 +66,6 @@ struct WalkArgs {
   float* max_out;      // E or D there, and of the state at each checkpoint: [.][head][pg],
   float* max_check;    // for the kernel that turns them into operands
   int pg;              // sixteens of headdim
-  const float* h0;     // reverse: initial states, or null, and
-  float* dot;          // their product with their gradient, [row][head][pg]
   float* fin;          // final state (forward) or gradient of the initial state (reverse), or null
   int64_t pv;          // row pitch of v
   int64_t pe;          // row pitch of E and D: headdim rounded up to fours

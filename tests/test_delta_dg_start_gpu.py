@@ -1,5 +1,5 @@
-"""dg of a row's first tokens where an initial state comes in: summed from the
-start, so what happens behind them does not reach its rounding."""
+"""dg of a row's first tokens where an initial state comes in: what happens
+behind them does not reach its rounding."""
 import pytest
 import torch
 

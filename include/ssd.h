@@ -504,7 +504,8 @@ SSD_API ssd_status ssd_bwd(const ssd_bwd_args* args, void* stream);
  * and the sums 32 in either type, and y is rounded once.  It equals the
  * recurrence up to rounding, which is relative to the largest magnitudes of a
  * token's q and k, and for each row of headdim of its state (some 2^-29 of the
- * row's largest value) and of a chunk's v - exp(g) S k.  Every
+ * row's largest value) and of a chunk's v - exp(g) S k.  Where g is above zero
+ * it grows with the exponential of its sums over 32 tokens.  Every
  * input must be finite, but for g, where -inf is a decay of zero: a value that
  * is not finite can make the outputs of its head from up to 31 tokens before
  * it undefined.  So padding should hold ordinary values (zeros, say; with g and

@@ -746,7 +746,8 @@ cudaError_t launch_row(const Args& a, cudaStream_t st, int* parts) {
 }
 
 // Rows that 16-byte packs do not divide, in pairs or single elements: half a
-// row to an eighth of the loads' width.
+// row to an eighth of the loads' width.  Up to 160 of them lie in one warp, five a
+// lane, and cost no barrier; then in a CTA of four, then eight a thread.
 template <typename T, int E, bool BWD>
 cudaError_t launch_narrow(const Args& a, cudaStream_t st, int* parts, bool* wide) {
   constexpr int kB = BWD ? 2 : 4;
@@ -763,7 +764,10 @@ cudaError_t launch_narrow(const Args& a, cudaStream_t st, int* parts, bool* wide
 }
 
 // The group by the row's packs: part of a warp up to 64 packs (no barrier),
-// else a CTA of as many threads as the row needs with one or two packs each.
+// else a CTA of as many threads as the row needs with one or two packs each.  The
+// steps between them are where a CTA's threads run out at the registers that its
+// packs take: 256 of one pack, 320 of two with two CTAs an SM left (three forward),
+// 512 of two with one.
 // `vec`: elements to which every row is aligned (E, 2 or 1).  Where a row's
 // registers or its ring end, at 1024 packs, 4096 pairs or 4096 single elements, it
 // is swept from memory.  In fp32 that puts aligned rows of 4100 to 8192 columns
